@@ -234,14 +234,17 @@ def _pow2(e):
 
 def _quantise(x):
     """e4m3 elements and exponent bytes of x [..., dh] in 32 bits: per block the least power of
-    two 2^e with |x| <= 448 * 2^e, and x * 2^-e (exact) rounded once."""
+    two 2^e with |x| <= 448 * 2^e, and x * 2^-e (exact) rounded once. A block with an infinity
+    or a NaN is stored as a whole as NaN: zeros under the exponent byte 255."""
     shape = x.shape
     x = x.reshape(*shape[:-1], -1, min(BLOCK, shape[-1]))
-    top = torch.where(torch.isfinite(x), x.abs(), 0.0).amax(-1, keepdim=True)
+    fine = torch.isfinite(x).all(-1, keepdim=True)
+    top = torch.where(fine, x, 0.0).abs().amax(-1, keepdim=True)
     mant, e = torch.frexp(top)                     # top = mant * 2^e, mant in [0.5, 1)
     e = e - 9 + (mant > E4M3_MAX / 512).to(e.dtype)
     e = torch.where(top > 0, e, E_MIN).clamp(min=E_MIN)
-    y = torch.where(torch.isfinite(x), x * _pow2(-e), math.nan)
+    y = torch.where(fine, x * _pow2(-e), 0.0)
+    e = torch.where(fine, e, 128)
     return (y.to(torch.float8_e4m3fn).reshape(shape).contiguous(),
             (e + 127).squeeze(-1).to(torch.uint8).contiguous())
 
