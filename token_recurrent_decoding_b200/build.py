@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,8 +27,9 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-    "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden",
 ]
+OBJ = os.path.join(PKG, "_build")  # one object and one dependency file per unit
 
 
 def sources():
@@ -45,14 +47,41 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _object(unit: str) -> str:
+    return os.path.join(OBJ, os.path.splitext(os.path.basename(unit))[0] + ".o")
+
+
+def _object_stale(unit: str) -> bool:
+    """Whether the unit's object is older than a file of this tree that its last compilation read."""
+    obj = _object(unit)
+    if not (os.path.exists(obj) and os.path.exists(obj + ".d")):
+        return True
+    with open(obj + ".d") as f:
+        deps = f.read().replace("\\\n", " ").split()[1:]
+    deps = [d for d in deps if os.path.abspath(d).startswith(ROOT + os.sep)] + [unit, __file__]
+    t = os.path.getmtime(obj)
+    return any(not os.path.exists(d) or os.path.getmtime(d) > t for d in deps)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Compile the units that changed, side by side, and link them."""
     if not force and not stale():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    todo = [u for u in units() if force or extra or _object_stale(u)]
+
+    def compile_unit(unit):
+        obj = _object(unit)
+        cmd = [NVCC, *FLAGS, *extra, "-MD", "-MF", obj + ".d", "-c", unit, "-o", obj + ".tmp"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+        os.replace(obj + ".tmp", obj)
+
+    with ThreadPoolExecutor(max(1, min(len(todo), os.cpu_count() or 1))) as pool:
+        list(pool.map(compile_unit, todo))
     tmp = LIB + ".tmp"
-    cmd = [NVCC, *FLAGS, *extra, *units(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+    subprocess.check_call([NVCC, *FLAGS, "-shared", *map(_object, units()), "-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
