@@ -508,6 +508,147 @@ RLT_API int rlt_attend_noalloc(const float *q, const void *kv, const int32_t *h_
                                int n_heads, int head_dim, int cap, int dtype, void *out,
                                rlt_stream stream);
 
+/* ------------------------------------------------------------ paged serving
+ * Keys and values kept in pages, a chunk of new tokens attending over them
+ * and drafted tokens verified against the target's distribution (no
+ * counterpart in the pages; the serving loop above handles one token per call
+ * against contiguous storage). A speculative step of a batch is:
+ * rlt_paged_append (the chunk's keys and values), rlt_attend_paged (its
+ * queries), the head's logits of its rows, rlt_verify; the caller then lowers
+ * each sequence's length to what was accepted, and the next append overwrites
+ * the refused rows.
+ *
+ * A cache, owned by the caller (one per layer):
+ *   pages   device, 16-byte aligned, [n_pages][n_kv_heads][2][page_size][head_dim]:
+ *           per page and head a key block, then a value block
+ *   scales  RLT_KV_E4M3 only (else NULL): device, 16-byte aligned, uint8
+ *           [n_pages][n_kv_heads][2][page_size][head_dim / B], B = min(32, head_dim)
+ *   page_size  a multiple of 16, at most 1024
+ *   head_dim   16, 32, 64 or 128
+ *   dtype   RLT_F32 or RLT_BF16: type of the rows that calls read and write
+ *   kind    RLT_KV_PLAIN: elements of `dtype`. RLT_KV_E4M3: 8-bit floats (four
+ *           exponent bits of bias 7, three of fraction, largest 448), each block
+ *           of B elements of a row under one power of two: scale byte b stands
+ *           for 2^(b - 127), an element's value is e4m3 * 2^(b - 127). Writing
+ *           takes the least power of two >= 2^-110 with max|x| <= 448 * 2^e, so
+ *           x * 2^-e is exact, each element is rounded once (to nearest, ties to
+ *           even), and what is stored is exact in bf16 and fp32. A block that
+ *           holds an infinity or a NaN is stored as NaN: zeros under scale byte
+ *           255. The element codes of NaN (0x7f, 0xff) are not written; in pages
+ *           from elsewhere they stand for +-480. Scale bytes from elsewhere: 17..187
+ *           or 255. */
+enum { RLT_KV_PLAIN = 0, RLT_KV_E4M3 = 1 };
+typedef struct rlt_paged_kv {
+  void *pages;
+  uint8_t *scales;
+  int n_pages, page_size, n_kv_heads, head_dim, dtype, kind;
+} rlt_paged_kv;
+
+/* Which rows a call is about, in device memory, read when the call runs (so a
+ * captured call follows later contents):
+ *   page_table [n][table_width]: page of positions p * page_size .. of sequence b
+ *   cu_rows    [n + 1], ascending from >= 0 to <= rows: sequence b owns rows
+ *              cu_rows[b] .. cu_rows[b + 1] - 1 of the call's dense buffers
+ *   kv_len     [n]: positions of sequence b, its rows of this call included; row
+ *              i of m is position kv_len - m + i
+ *   n          1 .. RLT_PAGED_MAX_SEQS (2048)
+ *   rows       rows of the dense buffers; those behind cu_rows[n] are not touched
+ *   status     NULL or a device int32 the kernels OR the bits below into. Nothing
+ *              outside the caller's buffers is read or written in any case. */
+#define RLT_PAGED_MAX_SEQS 2048
+enum {
+  RLT_PAGED_BAD_PAGE = 1, /* a needed page number is not 0 .. n_pages - 1, or a position lies
+                             before 0 or beyond the table: that row or key does not exist */
+  RLT_PAGED_BAD_ROWS = 2  /* cu_rows descends or passes `rows` (every row is then left
+                             as it was), or for rlt_attend_paged a sequence has more rows or positions than
+                             max_rows, max_len (its rows are left as they were) */
+};
+typedef struct rlt_paged_rows {
+  const int32_t *page_table;
+  int table_width;
+  const int32_t *cu_rows, *kv_len;
+  int n, rows;
+  int32_t *status;
+} rlt_paged_rows;
+
+/* Write the listed rows of k and v (device, cache->dtype, [rows][n_kv_heads][head_dim],
+ * row stride ld elements: the parts of a fused projection's output serve as they
+ * are) into the cache. A place that two listed rows share ends with either's
+ * elements, or a mix of both. Errors: INVALID_ARG (null pointers, sizes, ld below
+ * n_kv_heads * head_dim, k, v or ld not on 16-byte steps), UNSUPPORTED (head_dim). */
+RLT_API int rlt_paged_append(const rlt_paged_kv *cache, const rlt_paged_rows *where,
+                             const void *k, const void *v, int64_t ld, rlt_stream stream);
+
+/* The reverse: the listed rows as stored, in cache->dtype. A row that does not
+ * exist reads as zeros. cu_rows = the running sum of kv_len reads whole
+ * sequences. Errors as rlt_paged_append. */
+RLT_API int rlt_paged_read(const rlt_paged_kv *cache, const rlt_paged_rows *where, void *k,
+                           void *v, int64_t ld, rlt_stream stream);
+
+/* Bytes of device workspace rlt_attend_paged needs (0 if the shape is invalid). */
+RLT_API size_t rlt_attend_paged_workspace_bytes(const rlt_paged_kv *cache, int n, int n_heads,
+                                                int rows, int max_rows, int max_len);
+
+/* Attention of a chunk of new tokens over a paged cache that already holds
+ * their keys and values: the row at position p of a sequence and head h attends
+ * to keys max(0, p - window + 1) .. p of head h / (n_heads / n_kv_heads),
+ *   out = softmax(q . K_j / sqrt(head_dim)) V_j,  lse = log sum exp(q . K_j / sqrt(head_dim)).
+ *   q        device, cache->dtype, [rows][n_heads][head_dim], row stride ldq elements
+ *   out      device, cache->dtype, [rows][n_heads][head_dim], row stride ldo
+ *   lse      NULL or device float32 [rows][n_heads]
+ *   n_heads  a multiple of n_kv_heads
+ *   max_rows, max_len  host bounds of the rows and positions of one sequence; they
+ *            choose kernels and size the workspace
+ *   window   0: no limit
+ *   workspace device, 256-byte aligned, owned by the caller; calls that share one
+ *            must not overlap
+ * A row that sees no key gives zeros and -inf. What lies in keys and values that
+ * a row does not see never reaches it; a row that sees a value with an infinity
+ * or a NaN among keys that other rows of the chunk do not see becomes NaN. A
+ * row's result does not depend on the batch it is in. Errors: INVALID_ARG (null pointers, sizes,
+ * strides or alignment as rlt_paged_append), UNSUPPORTED (head_dim), CAPACITY
+ * (workspace too small). */
+RLT_API int rlt_attend_paged(const rlt_paged_kv *cache, const rlt_paged_rows *where,
+                             const void *q, int64_t ldq, int n_heads, int max_rows, int max_len,
+                             int window, void *out, int64_t ldo, float *lse, void *workspace,
+                             size_t workspace_bytes, rlt_stream stream);
+
+/* Bytes of device workspace rlt_verify needs (0 if the shape is invalid). */
+RLT_API size_t rlt_verify_workspace_bytes(int n, int k, int vocab);
+
+/* Verify up to k drafted tokens per sequence against the target's logits with
+ * given random numbers, so that what is emitted is distributed as the target's
+ * own draws. With p_i = softmax(target[b][i] / temperature) and q_i the same of
+ * draft[b][i] (draft NULL: q_i is one at the drafted token x_i, zero elsewhere):
+ *   token i = 0, 1, .. is accepted if uniforms[b][i] * q_i(x_i) < p_i(x_i);
+ *   at the first refusal i the new token is drawn from max(p_i - q_i, 0) (from p_i
+ *   where that leaves nothing), if none is refused from p_i behind the last one. The draw is the smallest v
+ *   whose cumulative weight exceeds uniforms[b][k] * (sum of weights).
+ * temperature 0: x_i is accepted if it is the target's first maximum, and the
+ * new token is that maximum (draft and uniforms unused). Tests and sums hold 64
+ * bits. NaN logits count as -inf (weight 0); where +inf occurs, those entries
+ * share the weight. A row without any weight has no token: it ends the
+ * sequence's answer there.
+ *   target   device float32, element (b, i, v) at b * target_seq + i * target_pos + v,
+ *            i = 0 .. k (rows behind a draft's end are not read)
+ *   draft    device float32, (b, i, v) at b * draft_seq + i * draft_pos + v, i = 0 .. k-1
+ *   draft_tokens device int32 [n][k]; one outside 0 .. vocab-1 ends the draft before it
+ *   draft_len  NULL (k each) or device int32 [n], clamped to 0 .. k
+ *   uniforms device float32 [n][k + 1] in [0, 1)
+ *   tokens   device int32 [n][k + 1]: accepted ones, the new one, then -1
+ *   counts   device int32 [n]: tokens emitted, accepted + 1 (accepted, if the
+ *            deciding row has no weight)
+ *   workspace device, 256-byte aligned, owned by the caller; calls that share one
+ *            must not overlap
+ * k 0 .. 32; draft, draft_tokens may be NULL if k = 0. Errors: INVALID_ARG,
+ * CAPACITY (workspace too small). */
+RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_pos,
+                       const float *draft, int64_t draft_seq, int64_t draft_pos,
+                       const int32_t *draft_tokens, const int32_t *draft_len, int n, int k,
+                       int vocab, float temperature, const float *uniforms, int32_t *tokens,
+                       int32_t *counts, void *workspace, size_t workspace_bytes,
+                       rlt_stream stream);
+
 /* Kernel classes reported by rlt_get_stats. */
 enum {
   RLT_K_XATTN = 0, /* decoder cross-attention over M<=t (split-KV + merge) */

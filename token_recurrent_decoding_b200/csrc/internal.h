@@ -18,4 +18,7 @@ int attend_run_internal(const float *q, const void *kv, const int32_t *h_lengths
 // Workspace bytes of the standalone decode attention (0: invalid shape).
 size_t attend_workspace_internal(int n, int H, int dh, int cap);
 
+// RLT_OK, or RLT_ERR_CUDA with the error noted for rlt_last_cuda_error.
+int cuda_status_internal(cudaError_t e, int line);
+
 }  // namespace rlt

@@ -1766,6 +1766,11 @@ int attend_run_internal(const float *q, const void *kv, const int32_t *h_lengths
   return attend_run(q, kv, h_lengths, n, H, dh, cap, dtype, out, workspace, workspace_bytes, st);
 }
 
+int cuda_status_internal(cudaError_t e, int line) {
+  note_error(e, line);
+  return cuda_status(e);
+}
+
 size_t attend_workspace_internal(int n, int H, int dh, int cap) {
   if (!attend_shape_ok(n, H, dh, cap)) return 0;
   return attend_ws_layout(n, H, dh, cap).total;

@@ -68,6 +68,21 @@ STEP_CHAIN, STEP_FUSED = 0, 1
 K_NAMES = ("xattn", "swa", "gemm", "other", "encoder", "step")
 
 
+class rlt_paged_kv(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("scales", C.c_void_p)] + [(n, C.c_int) for n in (
+        "n_pages", "page_size", "n_kv_heads", "head_dim", "dtype", "kind")]
+
+
+class rlt_paged_rows(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("table_width", C.c_int), ("cu_rows", C.c_void_p),
+                ("kv_len", C.c_void_p), ("n", C.c_int), ("rows", C.c_int),
+                ("status", C.c_void_p)]
+
+
+KV_PLAIN, KV_E4M3 = 0, 1
+PAGED_BAD_PAGE, PAGED_BAD_ROWS = 1, 2
+
+
 class rlt_stats(C.Structure):
     _fields_ = [("launches", C.c_int64), ("kernel_launches", C.c_int64 * 6),
                 ("kernel_ms", C.c_double * 6), ("kernel_bytes", C.c_double * 6),
@@ -116,6 +131,15 @@ def _declare(lib):
     lib.rlt_attend_workspace_bytes.argtypes = [I, I, I, I]
     lib.rlt_attend_workspace_bytes.restype = C.c_size_t
     lib.rlt_attend.argtypes = [P, P, P, I, I, I, I, I, P, P, C.c_size_t, P]
+    L, Z = C.c_int64, C.c_size_t
+    lib.rlt_paged_append.argtypes = [P, P, P, P, L, P]
+    lib.rlt_paged_read.argtypes = [P, P, P, P, L, P]
+    lib.rlt_attend_paged_workspace_bytes.argtypes = [P, I, I, I, I, I]
+    lib.rlt_attend_paged_workspace_bytes.restype = Z
+    lib.rlt_attend_paged.argtypes = [P, P, P, L, I, I, I, I, P, L, P, P, Z, P]
+    lib.rlt_verify_workspace_bytes.argtypes = [I, I, I]
+    lib.rlt_verify_workspace_bytes.restype = Z
+    lib.rlt_verify.argtypes = [P, L, L, P, L, L, P, P, I, I, I, C.c_float, P, P, P, P, Z, P]
     lib.rlt_profile.argtypes = [P, I]
     lib.rlt_get_stats.argtypes = [P, P]
     lib.rlt_status_string.argtypes = [I]
@@ -212,6 +236,237 @@ def attend(q, kv, lengths, out, workspace, stream=None):
                              dh, cap, dtype, C.c_void_p(out.data_ptr()),
                              C.c_void_p(workspace.data_ptr()), workspace.numel(),
                              _stream_handle(stream)), "rlt_attend")
+
+
+# ------------------------------------------------------------- paged serving
+def _need(ok: bool, what: str):
+    """Arguments the C ABI cannot see (types, shapes, devices of tensors)."""
+    if not ok:
+        raise RLTError(1, what)
+
+
+class _On:
+    """Runs a standalone call on a tensor's device: makes it current and yields the stream's
+    handle (the caller's stream, else the device's current one)."""
+
+    __slots__ = ("torch", "device", "stream", "before")
+
+    def __init__(self, device, stream):
+        import torch
+        self.torch, self.device, self.stream, self.before = torch, device, stream, None
+
+    def __enter__(self):
+        cuda = self.torch.cuda
+        if self.device.index != cuda.current_device():
+            self.before = cuda.current_device()
+            cuda.set_device(self.device)
+        s = self.stream if self.stream is not None else cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            self.torch.cuda.set_device(self.before)
+
+    def scratch(self, nbytes):
+        """Workspace of one call, kept from reuse until the call's stream has passed it."""
+        t = self.torch.empty(nbytes, dtype=self.torch.uint8, device=self.device)
+        if self.stream is not None:
+            t.record_stream(self.stream)
+        return t
+
+
+class PagedKV:
+    """A paged cache of keys and values (rlt_paged_kv) over the caller's tensors.
+
+    pages  [n_pages][n_kv_heads][2][page_size][head_dim], contiguous, on a GPU: float32 or
+           bfloat16 (kept as they are), or float8_e4m3fn (8 bits)
+    scales uint8 [n_pages][n_kv_heads][2][page_size][head_dim / min(32, head_dim)] for 8 bits
+    dtype  of the rows that calls read and write; for 8 bits bfloat16 unless given
+    """
+
+    def __init__(self, pages, scales=None, dtype=None):
+        import torch
+        _need(pages.is_cuda and pages.dim() == 5 and pages.shape[2] == 2
+              and pages.is_contiguous(), "PagedKV: pages")
+        e4 = pages.dtype == torch.float8_e4m3fn
+        dtype = dtype or (torch.bfloat16 if e4 else pages.dtype)
+        _need(dtype in (torch.float32, torch.bfloat16) and (e4 or dtype == pages.dtype),
+              "PagedKV: dtype")
+        n_pages, heads, _, page, dh = pages.shape
+        if e4:
+            _need(scales is not None and scales.dtype == torch.uint8 and scales.is_contiguous()
+                  and scales.device == pages.device
+                  and tuple(scales.shape) == (n_pages, heads, 2, page, dh // min(32, dh)),
+                  "PagedKV: scales")
+        else:
+            _need(scales is None, "PagedKV: scales of a cache that has none")
+        self.pages, self.scales, self.dtype, self.device = pages, scales, dtype, pages.device
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, heads, page, dh
+        self.kind = KV_E4M3 if e4 else KV_PLAIN
+        self._c = rlt_paged_kv(pages.data_ptr(), scales.data_ptr() if e4 else None, n_pages, page,
+                               heads, dh, BF16 if dtype == torch.bfloat16 else 0, self.kind)
+        self._ref = C.addressof(self._c)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=None, kind=KV_PLAIN,
+              device="cuda"):
+        """A new cache of uninitialised pages."""
+        import torch
+        dtype = dtype or torch.bfloat16
+        shape = (n_pages, n_kv_heads, 2, page_size, head_dim)
+        if kind == KV_PLAIN:
+            return cls(torch.empty(shape, dtype=dtype, device=device))
+        block = min(32, head_dim)
+        return cls(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(shape[:-1] + (head_dim // block,), dtype=torch.uint8,
+                               device=device), dtype)
+
+    def _rows(self, table, cu_rows, kv_len, rows, status, what):
+        import torch
+        i32, dev = torch.int32, self.device
+        n = kv_len.shape[0]
+        _need(table.dtype == i32 and table.dim() == 2 and table.shape[0] == n
+              and table.is_contiguous() and table.device == dev, what + ": page table")
+        _need(cu_rows.dtype == i32 and cu_rows.shape == (n + 1,) and cu_rows.is_contiguous()
+              and cu_rows.device == dev, what + ": cu_rows")
+        _need(kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.is_contiguous()
+              and kv_len.device == dev, what + ": kv_len")
+        if status is not None:
+            _need(status.dtype == i32 and status.numel() == 1 and status.device == dev,
+                  what + ": status")
+            status = status.data_ptr()
+        return rlt_paged_rows(table.data_ptr(), table.shape[1], cu_rows.data_ptr(),
+                              kv_len.data_ptr(), n, rows, status)
+
+    def _dense(self, x, heads, what):
+        """Row stride of a dense buffer [rows][heads][head_dim] whose rows may lie apart."""
+        _need(x.dtype == self.dtype and x.device == self.device and x.dim() == 3
+              and x.shape[1] == heads and x.shape[2] == self.head_dim, what)
+        s = x.stride()
+        _need(s[2] == 1 and (s[1] == self.head_dim or heads == 1), what)
+        return s[0] if x.shape[0] > 1 else max(s[0], heads * self.head_dim)
+
+
+def _paged_rows_call(fn, what, cache, table, k, v, cu_rows, kv_len, status, stream):
+    ld = cache._dense(k, cache.n_kv_heads, what + ": k")
+    _need(cache._dense(v, cache.n_kv_heads, what + ": v") == ld and v.shape == k.shape,
+          what + ": k and v of one shape and row stride")
+    r = cache._rows(table, cu_rows, kv_len, k.shape[0], status, what)
+    with _On(cache.device, stream) as st:
+        _check(fn(cache._ref, C.addressof(r), k.data_ptr(), v.data_ptr(), ld, st), what)
+
+
+def paged_append(cache: PagedKV, table, k, v, cu_rows, kv_len, status=None, stream=None):
+    """rlt_paged_append: rows of k, v [rows][n_kv_heads][head_dim] into the cache. table int32
+    [n][width], cu_rows int32 [n + 1], kv_len int32 [n] (these rows included), on the GPU."""
+    _paged_rows_call(_lib().rlt_paged_append, "rlt_paged_append", cache, table, k, v, cu_rows,
+                     kv_len, status, stream)
+
+
+def paged_read(cache: PagedKV, table, cu_rows, kv_len, k, v, status=None, stream=None):
+    """rlt_paged_read: the listed rows into k, v [rows][n_kv_heads][head_dim]."""
+    _paged_rows_call(_lib().rlt_paged_read, "rlt_paged_read", cache, table, k, v, cu_rows,
+                     kv_len, status, stream)
+
+
+def attend_paged_workspace_bytes(cache: PagedKV, n: int, n_heads: int, rows: int, max_rows: int,
+                                 max_len: int) -> int:
+    return int(_lib().rlt_attend_paged_workspace_bytes(cache._ref, n, n_heads, rows, max_rows,
+                                                       max_len))
+
+
+def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_len: int, out=None,
+                 lse=None, window: int = 0, workspace=None, status=None, stream=None):
+    """rlt_attend_paged: q [rows][n_heads][head_dim] over the cache -> out (allocated where None;
+    rows behind the last sequence are not written). lse: None or float32 [rows][n_heads]."""
+    import torch
+    what = "rlt_attend_paged"
+    _need(q.dim() == 3, what + ": q")
+    rows, heads = q.shape[0], q.shape[1]
+    ldq = cache._dense(q, heads, what + ": q")
+    on = _On(cache.device, stream)
+    if out is None:
+        out = torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
+        if stream is not None:
+            out.record_stream(stream)
+    ldo = cache._dense(out, heads, what + ": out")
+    _need(out.shape == q.shape, what + ": out")
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.shape == (rows, heads) and lse.is_contiguous()
+              and lse.device == cache.device, what + ": lse")
+    r = cache._rows(table, cu_rows, kv_len, rows, status, what)
+    if workspace is None:
+        workspace = on.scratch(attend_paged_workspace_bytes(cache, r.n, heads, rows, max_rows,
+                                                            max_len))
+    _need(workspace.device == cache.device and workspace.dtype == torch.uint8
+          and workspace.is_contiguous(), what + ": workspace")
+    with on as st:
+        _check(_lib().rlt_attend_paged(
+            cache._ref, C.addressof(r), q.data_ptr(), ldq, heads, max_rows, max_len, window,
+            out.data_ptr(), ldo, lse.data_ptr() if lse is not None else None,
+            workspace.data_ptr(), workspace.numel(), st), what)
+    return out
+
+
+def verify_workspace_bytes(n: int, k: int, vocab: int) -> int:
+    return int(_lib().rlt_verify_workspace_bytes(n, k, vocab))
+
+
+def verify(target, draft, draft_tokens, temperature: float, uniforms=None, draft_lengths=None,
+           tokens=None, counts=None, workspace=None, stream=None):
+    """rlt_verify: target float32 [n][k + 1][V] and draft float32 [n][k][V] (or None) in any strides
+    of their first two dimensions, draft_tokens int32 [n][k], uniforms float32 [n][k + 1],
+    draft_lengths int32 [n] or None -> (tokens int32 [n][k + 1], counts int32 [n])."""
+    import torch
+    what, dev = "rlt_verify", target.device
+    _need(target.is_cuda and target.dtype == torch.float32 and target.dim() == 3
+          and (target.stride(2) == 1 or target.shape[2] == 1), what + ": target")
+    n, k, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    ts = target.stride()
+    ds = (0, 0)
+    if draft is not None:
+        _need(draft.dtype == torch.float32 and draft.shape == (n, k, V) and draft.device == dev
+              and (draft.stride(2) == 1 or V == 1), what + ": draft")
+        ds = draft.stride()
+    _need(draft_tokens is None and k == 0 or draft_tokens is not None
+          and draft_tokens.dtype == torch.int32 and draft_tokens.shape == (n, k)
+          and draft_tokens.is_contiguous() and draft_tokens.device == dev,
+          what + ": draft_tokens")
+    _need(uniforms is None and temperature == 0 or uniforms is not None
+          and uniforms.dtype == torch.float32 and uniforms.shape == (n, k + 1)
+          and uniforms.is_contiguous() and uniforms.device == dev, what + ": uniforms")
+    if draft_lengths is not None:
+        _need(draft_lengths.dtype == torch.int32 and draft_lengths.shape == (n,)
+              and draft_lengths.is_contiguous() and draft_lengths.device == dev,
+              what + ": draft_lengths")
+    on = _On(dev, stream)
+    made = []
+    if tokens is None:
+        tokens = torch.empty((n, k + 1), dtype=torch.int32, device=dev)
+        made.append(tokens)
+    if counts is None:
+        counts = torch.empty(n, dtype=torch.int32, device=dev)
+        made.append(counts)
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    _need(tokens.dtype == torch.int32 and tokens.shape == (n, k + 1) and tokens.is_contiguous()
+          and tokens.device == dev, what + ": tokens")
+    _need(counts.dtype == torch.int32 and counts.shape == (n,) and counts.is_contiguous()
+          and counts.device == dev, what + ": counts")
+    if workspace is None:
+        workspace = on.scratch(verify_workspace_bytes(n, k, V))
+    _need(workspace.device == dev and workspace.dtype == torch.uint8
+          and workspace.is_contiguous(), what + ": workspace")
+    with on as st:
+        _check(_lib().rlt_verify(
+            target.data_ptr(), ts[0], ts[1], draft.data_ptr() if draft is not None else None,
+            ds[0], ds[1], draft_tokens.data_ptr() if k else None,
+            draft_lengths.data_ptr() if draft_lengths is not None else None, n, k, V,
+            float(temperature), uniforms.data_ptr() if uniforms is not None else None,
+            tokens.data_ptr(), counts.data_ptr(), workspace.data_ptr(), workspace.numel(), st),
+            what)
+    return tokens, counts
 
 
 class Model:
