@@ -559,9 +559,10 @@ typedef struct rlt_paged_kv {
 enum {
   RLT_PAGED_BAD_PAGE = 1, /* a needed page number is not 0 .. n_pages - 1, or a position lies
                              before 0 or beyond the table: that row or key does not exist */
-  RLT_PAGED_BAD_ROWS = 2  /* cu_rows descends or passes `rows` (every row is then left
+  RLT_PAGED_BAD_ROWS = 2, /* cu_rows descends or passes `rows` (every row is then left
                              as it was), or for rlt_attend_paged a sequence has more rows or positions than
                              max_rows, max_len (its rows are left as they were) */
+  RLT_PAGED_TIMEOUT = 4   /* a bounded wait gave up: results are unspecified */
 };
 typedef struct rlt_paged_rows {
   const int32_t *page_table;

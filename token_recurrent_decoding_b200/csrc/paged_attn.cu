@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "paged_attn.cuh"
+#include "paged_attn_tc.cuh"
 
 namespace rlt {
 namespace {
@@ -14,16 +15,36 @@ bool attn_shape_ok(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_
          (int64_t)max_rows * n_heads <= (1 << 28);
 }
 
+// Stacked rows per kv head from which a sequence goes to the tcgen05 kernel
+// (bf16 rows, head sizes 64 and 128).
+constexpr int WIDE_FROM = 33;
+int wide_from(const rlt_paged_kv *c) {
+  return c->dtype == RLT_BF16 && (c->head_dim == 64 || c->head_dim == 128) ? WIDE_FROM : 1 << 30;
+}
+
+int64_t most_splits(int max_len, int min_keys) {
+  const int64_t n = ((int64_t)max_len + PA_TK + min_keys - 1) / min_keys;
+  return n < PA_MAX_SPLITS ? n : PA_MAX_SPLITS;
+}
+
 // Partial rows the split rule can make: a sequence of m rows makes at most
-// m * heads * splits, with splits below PA_SPLIT_UNITS / units + 1 and units at
-// least m * heads / PA_UNIT_ROWS.
-int64_t partial_rows(int n, int n_heads, int rows, int max_len) {
-  int64_t most = (max_len + PA_TK + PA_MIN_KEYS - 1) / PA_MIN_KEYS;
-  if (most > PA_MAX_SPLITS) most = PA_MAX_SPLITS;
-  if (most <= 1) return 0;
-  const int64_t a = most * rows * n_heads;
-  const int64_t b = (int64_t)n * PA_SPLIT_UNITS * PA_UNIT_ROWS + (int64_t)rows * n_heads;
-  return a < b ? a : b;
+// m * heads * splits, with splits below units aimed at / own units + 1 and own
+// units at least m * heads / rows of a unit; only sequences the kernel takes
+// count.
+int64_t partial_rows(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows,
+                     int max_len) {
+  const int group = n_heads / c->n_kv_heads, wide = wide_from(c);
+  const int64_t cells = (int64_t)rows * n_heads;
+  int64_t a = most_splits(max_len, PA_MIN_KEYS) > 1 ? (int64_t)n * PA_SPLIT_UNITS * PA_UNIT_ROWS : 0;
+  int64_t b = 0;
+  if ((int64_t)max_rows * group >= wide && most_splits(max_len, PA_WIDE_KEYS) > 1) {
+    int64_t seqs = (int64_t)rows * group / wide;
+    if (seqs > n) seqs = n;
+    b = seqs * PA_WIDE_UNITS * PA_WIDE_ROWS;
+  }
+  if (a + b == 0) return 0;
+  const int64_t all = most_splits(max_len, PA_MIN_KEYS) * cells;
+  return a + b + cells < all ? a + b + cells : all;
 }
 
 size_t workspace_bytes_of(int dh, int64_t part_rows) {
@@ -65,6 +86,20 @@ template <int KIND> cudaError_t launch_attn(const AttnArgs &A, int dh, int sms, 
   }
 }
 
+template <bool E4, int DH>
+cudaError_t launch_wide_kernel(const AttnArgs &A, int sms, cudaStream_t st) {
+  using Cfg = PwCfg<DH>;
+  const cudaError_t e = ensure_smem_limit(k_pattn_wide<E4, DH>, Cfg::bytes(RLT_PAGED_MAX_SEQS));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_pattn_wide<E4, DH>, sms, PW_THREADS, Cfg::bytes(A.R.n), st, A);
+}
+
+cudaError_t launch_wide(const AttnArgs &A, bool e4, int dh, int sms, cudaStream_t st) {
+  if (dh == 64)
+    return e4 ? launch_wide_kernel<true, 64>(A, sms, st) : launch_wide_kernel<false, 64>(A, sms, st);
+  return e4 ? launch_wide_kernel<true, 128>(A, sms, st) : launch_wide_kernel<false, 128>(A, sms, st);
+}
+
 template <typename T>
 cudaError_t launch_merge(const AttnArgs &A, int dh, int sms, cudaStream_t st) {
   const int64_t warps = (int64_t)A.R.rows * A.heads;
@@ -88,7 +123,8 @@ extern "C" {
 RLT_API size_t rlt_attend_paged_workspace_bytes(const rlt_paged_kv *cache, int n, int n_heads,
                                                 int rows, int max_rows, int max_len) {
   if (!attn_shape_ok(cache, n, n_heads, rows, max_rows, max_len)) return 0;
-  return workspace_bytes_of(cache->head_dim, partial_rows(n, n_heads, rows, max_len));
+  return workspace_bytes_of(cache->head_dim,
+                            partial_rows(cache, n, n_heads, rows, max_rows, max_len));
 }
 
 RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, const void *q,
@@ -104,7 +140,7 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
       !dense_rows_ok(out, ldo, n_heads, c->head_dim, c->dtype) || !workspace ||
       ((uintptr_t)workspace & 255) || ((uintptr_t)lse & 3))
     return RLT_ERR_INVALID_ARG;
-  const int64_t parts = partial_rows(w->n, n_heads, w->rows, max_len);
+  const int64_t parts = partial_rows(c, w->n, n_heads, w->rows, max_rows, max_len);
   if (workspace_bytes < workspace_bytes_of(c->head_dim, parts)) return RLT_ERR_CAPACITY;
   AttnArgs A;
   A.C = paged_view(c);
@@ -122,7 +158,8 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
   A.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->head_dim));
   A.part = static_cast<float *>(workspace);
   A.part_rows = (int)parts;
-  A.wide_from = 1 << 30;
+  A.wide_from = wide_from(c);
+  A.follows = 1;
   cudaStream_t st = (cudaStream_t)stream;
   const int sms = sm_count(), dh = c->head_dim;
   const bool e4 = c->kind == RLT_KV_E4M3;
@@ -132,6 +169,8 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
     e = e4 ? launch_attn<PA_E4M3>(A, dh, sms, st) : launch_attn<PA_BF16>(A, dh, sms, st);
   else
     e = e4 ? launch_attn<PA_E4M3_F32>(A, dh, sms, st) : launch_attn<PA_F32>(A, dh, sms, st);
+  if (e == cudaSuccess && (int64_t)max_rows * A.group >= A.wide_from)
+    e = launch_wide(A, e4, dh, sms, st);
   if (e == cudaSuccess && parts > 0)
     e = c->dtype == RLT_BF16 ? launch_merge<bf16>(A, dh, sms, st)
                              : launch_merge<float>(A, dh, sms, st);

@@ -41,6 +41,11 @@ constexpr int PA_UNIT_ROWS = 32;     // rows of a unit in the split rule
 constexpr int PA_SPLIT_UNITS = 256;  // units x splits aimed at per sequence
 constexpr int PA_MAX_SPLITS = 16;
 constexpr int PA_MIN_KEYS = 256;     // least keys of a split
+// The same of sequences that go to the tcgen05 kernel: tiles of 256 rows, one
+// CTA per SM, splits long enough that writing O in fp32 stays below a tenth.
+constexpr int PA_WIDE_ROWS = 256;
+constexpr int PA_WIDE_UNITS = 148;
+constexpr int PA_WIDE_KEYS = 4096;
 
 // How one sequence is cut, from its own rows and length only.
 struct SeqCut {
@@ -51,7 +56,8 @@ struct SeqCut {
 
 __device__ __host__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_heads, int window) {
+__device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_heads, int window,
+                                          bool wide) {
   SeqCut s;
   s.m = m;
   s.first = len - m;
@@ -59,8 +65,9 @@ __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_head
   const int lo = window > 0 ? max(0, max(s.first, 0) - window + 1) : 0;
   s.k_lo = min(lo, s.k_hi) & ~(PA_TK - 1);
   const int span = s.k_hi - s.k_lo;
-  const int units = max(1, kv_heads * ceil_div(m * group, PA_UNIT_ROWS));
-  int n = min(min(PA_MAX_SPLITS, ceil_div(PA_SPLIT_UNITS, units)), ceil_div(span, PA_MIN_KEYS));
+  const int units = max(1, kv_heads * ceil_div(m * group, wide ? PA_WIDE_ROWS : PA_UNIT_ROWS));
+  int n = min(min(PA_MAX_SPLITS, ceil_div(wide ? PA_WIDE_UNITS : PA_SPLIT_UNITS, units)),
+              ceil_div(span, wide ? PA_WIDE_KEYS : PA_MIN_KEYS));
   n = max(n, 1);
   s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);
   s.splits = max(1, ceil_div(span, s.keys));
@@ -79,7 +86,8 @@ struct AttnArgs {
   float scale_log2;  // log2(e) / sqrt(head_dim)
   float *part;       // [part_rows][DH + 2]: O (not divided), maximum (base 2), sum
   int part_rows;
-  int wide_from;     // sequences with this many (row, head in group) rows go to the wide kernel
+  int wide_from;     // sequences with this many stacked rows per kv head go to k_pattn_wide
+  int follows;       // k_pattn_wide: k_pattn of the same call runs before it
 };
 
 // Rows and cut of sequence b; rows 0 where it takes no part in the call, `fine`
@@ -92,12 +100,12 @@ __device__ __forceinline__ SeqCut cut_of(const AttnArgs &A, int b, int &row0, in
     const int len = A.R.len[b];
     if (hi - lo <= A.max_rows && len >= 0 && len <= A.max_len) {
       row0 = lo;
-      return cut_seq(hi - lo, len, A.group, A.C.H, A.window);
+      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, (hi - lo) * A.group >= A.wide_from);
     }
     flag_rows(A.R, RLT_PAGED_BAD_ROWS);
   }
   row0 = 0;
-  return cut_seq(0, 0, A.group, A.C.H, A.window);
+  return cut_seq(0, 0, A.group, A.C.H, A.window, false);
 }
 
 // Running sums over the sequences, in shared memory: items[b] items and

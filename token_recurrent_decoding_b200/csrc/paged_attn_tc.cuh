@@ -1,0 +1,701 @@
+// Chunk attention over a paged cache on the tcgen05 tensor cores: sequences
+// with many query rows per key head, bf16 queries, head sizes 64 and 128.
+//
+// An item is (sequence, kv head, 256 stacked query rows, range of keys), two
+// tiles of 128 rows that share every key tile of 128 positions. One CTA per
+// SM walks the items:
+//   warps 0-3, 4-7  softmax of row tile 0, 1: a thread per row (tensor-memory
+//                   lane = row)
+//   warps 8-11      loaders: queries, keys, values into shared memory in the
+//                   128-byte swizzle the MMA reads; bf16 rows with cp.async,
+//                   8-bit rows through registers as bf16 values
+//   warp 12         one lane issues tcgen05.mma
+// S_t = Q_t K^T goes to tensor memory (128 x 128 fp32); the softmax writes P
+// over it as bf16 (packed two keys a column), and O_t += P_t V takes P from
+// tensor memory and V as an MN-major operand as it lies in the cache. The
+// issue order PV_0(i), S_0(i+1), PV_1(i), S_1(i+1) lets one tile's softmax run
+// under the other tile's products.
+//
+// Softmax: O is rescaled (in tensor memory, by the softmax warps) only when a
+// row's maximum has grown by more than 2^8 since the reference it is scaled
+// by; until then weights of up to 2^8 stay exact enough (bf16 has the range,
+// the sum is fp32) and the join divides by the same reference. P's rounding to
+// bf16 is the precision of the matrix operand; sums take the unrounded weights.
+//
+// Values that some row of the tile does not see are cleared of infinities and
+// NaN by the loaders (0 * NaN would reach that row); a row that does see such
+// a key turns to NaN through its sum.
+//
+// Every mbarrier wait is bounded in device time; a CTA that gives up sets
+// RLT_PAGED_TIMEOUT and leaves.
+#pragma once
+
+#include "enc_attn.cuh"
+#include "gemm_tc.cuh"
+#include "paged_attn.cuh"
+
+namespace rlt {
+
+constexpr int PW_THREADS = 416, PW_LOADERS = 128;
+constexpr int PW_TK = 128;                // keys of a tile
+constexpr int PW_RT = 256;                // query rows of an item
+
+template <int DH> struct PwCfg {
+  static constexpr int STAGES = DH == 64 ? 4 : 2;  // of K and of V
+  static constexpr int HALF = 128 * 128;           // 128 rows of 64 entries
+  static constexpr int TILE = HALF * (DH / 64);
+  static constexpr int INFO = 2 * STAGES;          // key tiles whose flags are kept
+  static constexpr int Q = 0;
+  static constexpr int K = 2 * TILE;
+  static constexpr int V = K + STAGES * TILE;
+  static constexpr int BARS = V + STAGES * TILE;
+  static constexpr int NBARS = 2 + 4 * STAGES + 6;
+  static constexpr int FLAGS = BARS + NBARS * 8;   // [INFO][8] words: unseen keys, strange keys
+  static constexpr int SLOT = FLAGS + INFO * 8 * 4;
+  static constexpr int PLAN = SLOT + 16;
+  static int bytes(int n) { return PLAN + 2 * (n + 1) * 4 + 1024; }
+};
+
+__device__ __forceinline__ bool pw_wait(uint64_t *bar, unsigned parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    const bool done = mbar_test_wait(bar, parity);
+    if (__all_sync(FULL_MASK, done)) return true;
+    if (__shfl_sync(FULL_MASK, globaltimer_ns() - t0 > WAIT_LIMIT_NS_TC, 0)) return false;
+  }
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// V: rows of 128 bytes along the keys, 8-key groups 1024 bytes apart, the
+// second 64 head entries one half tile further.
+__device__ __forceinline__ uint64_t pw_desc_v(uint32_t addr, int half) {
+  uint64_t d = 0;
+  d |= (uint64_t)(addr >> 4) & 0x3FFFull;
+  d |= (uint64_t)(half >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void pw_ld32(uint32_t taddr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void pw_st32(uint32_t taddr, const uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void pw_st16(uint32_t taddr, const uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void pw_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void pw_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void pw_fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+// Two fp32 multiply-adds, two additions.
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+        "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+
+// Byte offset of 16-byte piece c of a row's 64 entries in a half tile.
+__device__ __forceinline__ int pw_piece(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
+
+// What every role needs of an item.
+struct PwItem {
+  SeqCut S;
+  int b, row0, kvh, split, r0, R;  // R: rows of the item
+  int k0, k1, nk;                  // first key, end, key tiles
+};
+
+__device__ __forceinline__ bool pw_item(const AttnArgs &A, const int *items, const int *parts,
+                                        int it, PwItem &I) {
+  I.b = find_seq(items, A.R.n, it);
+  int fine;
+  I.S = cut_of(A, I.b, I.row0, fine);
+  const int rows = I.S.m * A.group, tiles = ceil_div(rows, PW_RT);
+  int j = it - items[I.b];
+  const int rt = j % tiles;
+  j /= tiles;
+  I.split = j % I.S.splits;
+  I.kvh = j / I.S.splits;
+  I.r0 = rt * PW_RT;
+  I.R = min(PW_RT, rows - I.r0);
+  const int pos_lo = I.S.first + I.r0 / A.group, pos_hi = I.S.first + (I.r0 + I.R - 1) / A.group;
+  int k0 = I.S.k_lo + I.split * I.S.keys, k1 = min(I.S.k_hi, k0 + I.S.keys);
+  if (A.window > 0) k0 = max(k0, (pos_lo - A.window + 1) & ~(PA_TK - 1));
+  k1 = min(k1, pos_hi + 1);
+  I.k0 = k0;
+  I.k1 = k1;
+  I.nk = k1 > k0 ? ceil_div(k1 - k0, PW_TK) : 0;
+  return !(I.S.splits > 1 && parts[I.b + 1] > A.part_rows);
+}
+
+// Whether rows at positions lo .. hi all see keys key0 .. key0 + 127.
+__device__ __forceinline__ bool pw_all_see(const AttnArgs &A, const PwItem &I, int key0, int lo,
+                                           int hi) {
+  return key0 + PW_TK - 1 <= lo && key0 + PW_TK <= I.k1 &&
+         (A.window == 0 || key0 > hi - A.window);
+}
+
+template <bool E4, int DH>
+__global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) {
+  using Cfg = PwCfg<DH>;
+  constexpr int ST = Cfg::STAGES;
+  extern __shared__ uint8_t pw_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(pw_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::BARS);
+  uint64_t *q_full = bars, *q_empty = bars + 1, *k_full = bars + 2, *k_empty = k_full + ST,
+           *v_full = k_empty + ST, *v_empty = v_full + ST, *s_full = v_empty + ST,
+           *p_full = s_full + 2, *o_full = p_full + 2;
+  uint32_t *flags = reinterpret_cast<uint32_t *>(sm + Cfg::FLAGS);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Cfg::SLOT);
+  int *items = reinterpret_cast<int *>(sm + Cfg::PLAN), *parts = items + A.R.n + 1;
+  __shared__ int s_fail;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    s_fail = 0;
+    mbar_init(q_full, PW_LOADERS);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < ST; i++) {
+      mbar_init(k_full + i, PW_LOADERS);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, PW_LOADERS);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int t = 0; t < 2; t++) {
+      mbar_init(s_full + t, 1);
+      mbar_init(p_full + t, 128);
+      mbar_init(o_full + t, 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  // behind k_pattn the predecessors' writes are complete (it waited before it
+  // let this kernel start) and its own are waited for at the end
+  if (!A.follows) pdl_wait();
+  pdl_trigger();
+  scan_seqs<PW_THREADS>(A, items, parts, [&](const SeqCut &s) {
+    return s.m * A.group >= A.wide_from ? A.C.H * s.splits * ceil_div(s.m * A.group, PW_RT) : 0;
+  });
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = items[A.R.n];
+  volatile int *fail = &s_fail;
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------- loaders
+    const int tid = threadIdx.x - 256;
+    uint32_t n_item = 0, n_tile = 0;  // items and key tiles so far (barrier phases)
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
+      PwItem I;
+      if (!pw_item(A, items, parts, it, I)) {
+        if (tid == 0) flag_rows(A.R, RLT_PAGED_BAD_ROWS);
+        continue;
+      }
+      if (I.nk == 0) continue;
+      const int pos_lo = I.S.first + I.r0 / A.group,
+                pos_hi = I.S.first + (I.r0 + I.R - 1) / A.group;
+      if (n_item > 0 && !pw_wait(q_empty, (n_item - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      for (int x = tid; x < PW_RT * (DH / 8); x += PW_LOADERS) {
+        const int r = x / (DH / 8), c = x % (DH / 8);
+        if (I.R <= 128 && r >= 128) break;
+        const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
+        const bf16 *src = static_cast<const bf16 *>(A.q) +
+                          (r < I.R ? (int64_t)(I.row0 + tok) * A.ldq + head * DH + c * 8 : 0);
+        cp_async16(smem_u32(sm + Cfg::Q + (r >> 7) * Cfg::TILE + (c >> 3) * Cfg::HALF +
+                            pw_piece(r & 127, c & 7)),
+                   src, r < I.R ? 16 : 0);
+      }
+      cp_async_commit();
+
+      // pages of a key tile: lane j < 8 holds that of keys 16 j .. 16 j + 15
+      auto pages_of = [&](int i) {
+        int pid = -1;
+        const int key = I.k0 + i * PW_TK + (lane & 7) * PA_TK;
+        if (lane < 8 && key < I.k1) {
+          const int idx = key / A.C.P;
+          if (idx < A.R.width) pid = A.R.table[(size_t)I.b * A.R.width + idx];
+          if (pid < 0 || pid >= A.C.n_pages) {
+            pid = -1;
+            flag_rows(A.R, RLT_PAGED_BAD_PAGE);
+          }
+        }
+        return pid;
+      };
+      // row (of positions) of the cache's key plane that holds key (page pid >= 0)
+      auto cell_of = [&](int pid, int key) {
+        return ((size_t)pid * A.C.H + I.kvh) * 2 * A.C.P + key % A.C.P;
+      };
+      // flags of tile i: keys that do not exist, keys whose values were cleared
+      auto flag_word = [&](int i, int w) -> uint32_t * {
+        return flags + ((n_tile + i) % Cfg::INFO) * 8 + w;
+      };
+
+      if constexpr (!E4) {
+        // unit 0: Q; 1 + 2 i: K of tile i; 2 + 2 i: V of tile i. A unit is one
+        // cp.async group; it is handed on two units later, or at once when the
+        // loader would block on a stage that is still read.
+        constexpr int PASSES = DH / 8;             // 128 * DH / 8 pieces by 128 threads
+        constexpr int RPP = 128 / (DH / 8);        // rows of a pass: 8 or 16
+        int issued = 1, handed = 0;
+        uint64_t absent = 0;  // 8 bits a tile: 16-key groups without a page
+        auto hand = [&]() {
+          const int u = handed++;
+          if (u == 0) {
+            pw_fence_async();
+            tc_mbar_arrive(q_full);
+            return;
+          }
+          const int i = (u - 1) >> 1, st = (n_tile + i) % ST;
+          if (u & 1) {
+            pw_fence_async();
+            tc_mbar_arrive(k_full + st);
+            return;
+          }
+          const int key0 = I.k0 + i * PW_TK;
+          const uint32_t gone = (uint32_t)(absent >> (8 * (i & 7))) & 0xffu;
+          if (gone || !pw_all_see(A, I, key0, pos_lo, pos_hi)) {
+            if (tid < 4) {
+              // two groups of 16 keys a word
+              const uint32_t g2 = gone >> (2 * tid);
+              *flag_word(i, tid) = ((g2 & 1) ? 0xffffu : 0u) | ((g2 & 2) ? 0xffff0000u : 0u);
+              *flag_word(i, 4 + tid) = 0;
+            }
+            asm volatile("bar.sync 1, 128;\n" ::: "memory");
+#pragma unroll 1
+            for (int p = 0; p < PASSES; p++) {
+              const int row = p * RPP + tid / (DH / 8), c = tid % (DH / 8);
+              uint4 *v = reinterpret_cast<uint4 *>(sm + Cfg::V + st * Cfg::TILE +
+                                                   (c >> 3) * Cfg::HALF + pw_piece(row, c & 7));
+              const uint4 x = *v;
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              bool bad = false;
+#pragma unroll
+              for (int y = 0; y < 4; y++)
+                bad |= (w[y] & 0x7f80u) == 0x7f80u || (w[y] & 0x7f800000u) == 0x7f800000u;
+              if (bad) {
+                *v = make_uint4(0, 0, 0, 0);
+                atomicOr(flag_word(i, 4 + (row >> 5)), 1u << (row & 31));
+              }
+            }
+          } else if (tid < 8) {
+            *flag_word(i, tid) = 0;
+          }
+          pw_fence_async();
+          tc_mbar_arrive(v_full + st);
+        };
+        auto hand_all = [&]() {
+          cp_async_wait<0>();
+          while (handed < issued) hand();
+        };
+        int pid = pages_of(0);
+        for (int i = 0; ok && i < I.nk; i++) {
+          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
+          const int key0 = I.k0 + i * PW_TK;
+          const int pid_next = i + 1 < I.nk ? pages_of(i + 1) : -1;
+          const unsigned gone =
+              __ballot_sync(FULL_MASK, lane < 8 && pid < 0 && key0 + lane * PA_TK < I.k1) & 0xffu;
+          absent = (absent & ~((uint64_t)0xff << (8 * (i & 7)))) | (uint64_t)gone << (8 * (i & 7));
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++) {
+            uint64_t *empty = (kv ? v_empty : k_empty) + st;
+            if (use > 0) {
+              if (!__all_sync(FULL_MASK, mbar_test_wait(empty, (use - 1) & 1))) hand_all();
+              if (!pw_wait(empty, (use - 1) & 1)) {
+                ok = false;
+                break;
+              }
+            }
+            const uint32_t dst = smem_u32(sm + (kv ? Cfg::V : Cfg::K) + st * Cfg::TILE);
+            const int c = tid % (DH / 8);
+#pragma unroll 8
+            for (int p = 0; p < PASSES; p++) {
+              const int row = p * RPP + tid / (DH / 8), key = key0 + row;
+              const int pg = __shfl_sync(FULL_MASK, pid, p * RPP / PA_TK);
+              const bool on = pg >= 0 && key < I.S.k_hi;
+              const bf16 *src = reinterpret_cast<const bf16 *>(A.C.pages) +
+                                (on ? (cell_of(pg, key) + (kv ? A.C.P : 0)) * DH + c * 8 : 0);
+              cp_async16(dst + (c >> 3) * Cfg::HALF + pw_piece(row, c & 7), src, on ? 16 : 0);
+            }
+            cp_async_commit();
+            issued++;
+            if (issued - handed > 2) {
+              cp_async_wait<2>();
+              hand();
+            }
+          }
+          pid = pid_next;
+        }
+        hand_all();
+      } else {
+        cp_async_wait<0>();
+        pw_fence_async();
+        tc_mbar_arrive(q_full);
+        // codes through registers: the next unit's are fetched before this
+        // thread waits for its stage
+        constexpr int CPR = DH / 16;               // pieces of 16 codes of a row
+        constexpr int RPP = 128 / CPR;             // rows of a pass: 16 or 32
+        constexpr int PASSES = 128 / RPP;
+        constexpr int SB = DH / 32;
+        uint4 code[PASSES];
+        uint32_t sbyte[PASSES];
+        const int c = tid % CPR, row_in = tid / CPR;
+        int pid = -1;
+        uint32_t gone = 0;
+        auto fetch = [&](int i, int kv) {
+          const int key0 = I.k0 + i * PW_TK;
+          if (kv == 0) {
+            pid = pages_of(i);
+            gone = __ballot_sync(FULL_MASK, lane < 8 && pid < 0 && key0 + lane * PA_TK < I.k1) &
+                   0xffu;
+          }
+#pragma unroll
+          for (int p = 0; p < PASSES; p++) {
+            const int row = p * RPP + row_in, key = key0 + row;
+            const int pg = __shfl_sync(FULL_MASK, pid, row / PA_TK);
+            const bool on = pg >= 0 && key < I.S.k_hi;
+            const size_t cell = on ? cell_of(pg, key) + (kv ? A.C.P : 0) : 0;
+            code[p] = make_uint4(0, 0, 0, 0);
+            sbyte[p] = 127;
+            if (on) {
+              code[p] = *reinterpret_cast<const uint4 *>(A.C.pages + cell * DH + c * 16);
+              sbyte[p] = A.C.scales[cell * SB + c / 2];
+            }
+          }
+        };
+        fetch(0, 0);
+        for (int i = 0; ok && i < I.nk; i++) {
+          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
+          const int key0 = I.k0 + i * PW_TK;
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++) {
+            if (use > 0 && !pw_wait((kv ? v_empty : k_empty) + st, (use - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            const bool masked = kv == 1 && (gone || !pw_all_see(A, I, key0, pos_lo, pos_hi));
+            if (masked) {
+              if (tid < 4) {
+                const uint32_t g2 = gone >> (2 * tid);
+                *flag_word(i, tid) = ((g2 & 1) ? 0xffffu : 0u) | ((g2 & 2) ? 0xffff0000u : 0u);
+                *flag_word(i, 4 + tid) = 0;
+              }
+              asm volatile("bar.sync 1, 128;\n" ::: "memory");
+            } else if (kv == 1 && tid < 8) {
+              *flag_word(i, tid) = 0;
+            }
+            uint8_t *dst = sm + (kv ? Cfg::V : Cfg::K) + st * Cfg::TILE + (c >> 2) * Cfg::HALF;
+#pragma unroll
+            for (int p = 0; p < PASSES; p++) {
+              const int row = p * RPP + row_in;
+              if (masked && sbyte[p] == 255) {
+                atomicOr(flag_word(i, 4 + (row >> 5)), 1u << (row & 31));
+                sbyte[p] = 127;  // its codes are zeros
+              }
+              const uint32_t sc = scale_pair(sbyte[p], sbyte[p]);
+              const uint32_t w[4] = {code[p].x, code[p].y, code[p].z, code[p].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int y = 0; y < 4; y++) {
+                // codes 0, 2 and 1, 3 of the word, then put in order
+                const uint32_t even = e4m3x2_value(w[y] << 8, sc), odd = e4m3x2_value(w[y], sc);
+                o[2 * y] = __byte_perm(even, odd, 0x5410);
+                o[2 * y + 1] = __byte_perm(even, odd, 0x7632);
+              }
+              const int c8 = (c & 3) * 2;
+              *reinterpret_cast<uint4 *>(dst + pw_piece(row, c8)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(dst + pw_piece(row, c8 + 1)) =
+                  make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            pw_fence_async();
+            tc_mbar_arrive((kv ? v_full : k_full) + st);
+            if (kv == 0)
+              fetch(i, 1);
+            else if (i + 1 < I.nk)
+              fetch(i + 1, 0);
+          }
+        }
+      }
+      n_item++;
+      n_tile += I.nk;
+    }
+    if (!ok) *fail = 1;
+  } else if (warp == 12) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(128, PW_TK);
+      constexpr uint32_t idO = idesc_bf16_f32(128, DH) | (1u << 16);  // V: MN-major
+      uint32_t n_item = 0, n_tile = 0, n_t[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, unsigned parity) {
+        if (ok && !mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS_TC)) ok = false;
+        tc_fence_after();
+        return ok;
+      };
+      auto scores = [&](int t, int i) {
+        const uint64_t qd = smem_desc_sw128(sm + Cfg::Q + t * Cfg::TILE);
+        const uint64_t kd = smem_desc_sw128(sm + Cfg::K + ((n_tile + i) % ST) * Cfg::TILE);
+#pragma unroll
+        for (int k = 0; k < DH / 16; k++) {
+          const uint64_t at = (uint64_t)(k >> 2) * (Cfg::HALF >> 4) + 2 * (k & 3);
+          umma_bf16(tmem + t * 128, qd + at, kd + at, idS, k > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full + t);
+      };
+      for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
+        PwItem I;
+        if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
+        const int nt = I.R > 128 ? 2 : 1;
+        if (!wait(q_full, n_item & 1)) break;
+        for (int i = 0; ok && i <= I.nk; i++) {
+          // PV of tile i - 1 and the scores of tile i, row tile by row tile
+          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
+          const int pst = (n_tile + i + ST - 1) % ST, puse = (n_tile + i - 1) / ST;
+          if (i < I.nk && !wait(k_full + st, use & 1)) break;
+          if (i > 0 && !wait(v_full + pst, puse & 1)) break;
+          for (int t = 0; t < nt; t++) {
+            if (i > 0) {
+              if (!wait(p_full + t, (n_t[t] + i - 1) & 1)) break;
+              const uint32_t v0 = smem_u32(sm + Cfg::V + pst * Cfg::TILE);
+#pragma unroll
+              for (int k = 0; k < PW_TK / 16; k++)
+                umma_ts(tmem + 256 + t * DH, tmem + t * 128 + k * 8,
+                        pw_desc_v(v0 + k * 2048, Cfg::HALF), idO, (i > 1 || k > 0) ? 1u : 0u);
+              umma_commit(o_full + t);
+            }
+            if (i < I.nk) scores(t, i);
+          }
+          if (!ok) break;
+          if (i < I.nk) umma_commit(k_empty + st);
+          if (i > 0) umma_commit(v_empty + pst);
+          if (i + 1 == I.nk) umma_commit(q_empty);
+        }
+        n_item++;
+        n_tile += I.nk;
+        for (int t = 0; t < nt; t++) n_t[t] += I.nk;
+      }
+      if (!ok) *fail = 1;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tO = tmem + 256 + t * DH + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t n_tile = 0, n_t = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
+      PwItem I;
+      if (!pw_item(A, items, parts, it, I)) continue;
+      const int r = t * 128 + row;  // row of the item
+      const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
+      const int pos = r < I.R ? I.S.first + tok : -1;
+      const int pos_lo = I.S.first + (I.r0 + t * 128) / A.group;
+      const int pos_hi = I.S.first + (I.r0 + min(I.R, t * 128 + 128) - 1) / A.group;
+      if (t * 128 >= I.R) {  // no second tile: the whole warpgroup skips
+        n_tile += I.nk;
+        continue;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < I.nk; i++) {
+        const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
+        const int key0 = I.k0 + i * PW_TK;
+        if (!pw_wait(v_full + st, use & 1) || !pw_wait(s_full + t, (n_t + i) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
+        const bool all = pw_all_see(A, I, key0, pos_lo, pos_hi) &&
+                         !(fl[0] | fl[1] | fl[2] | fl[3]);
+        // the row's maximum
+        float mx = -INFINITY;
+        uint32_t s[32];
+        if (all) {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            pw_ld32(tS + 32 * c, s);
+            pw_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e++) mx = fmaxf(mx, __uint_as_float(s[e]));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            // keys of the chunk the row sees, as bits
+            const int k0 = key0 + 32 * c;
+            const int hi = min(min(pos, I.k1 - 1) - k0, 31);                // last seen
+            const int lo = A.window > 0 ? max(pos - A.window + 1 - k0, 0) : 0;  // first seen
+            uint32_t see = hi < 0 || lo > 31 ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+            see &= ~fl[c];
+            if (see & fl[4 + c]) l = NAN;
+            pw_ld32(tS + 32 * c, s);
+            pw_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e++) {
+              if (!(see >> e & 1)) s[e] = 0xff800000u;
+              mx = fmaxf(mx, __uint_as_float(s[e]));
+            }
+            pw_st32(tS + 32 * c, s);
+          }
+          pw_wait_st();
+        }
+        mx *= A.scale_log2;
+        // O keeps its reference until the maximum has outgrown it by 2^8
+        const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+        if (i > 0 && __any_sync(FULL_MASK, grow)) {
+          if (!pw_wait(o_full + t, (n_t + i - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float corr = grow ? pa_exp2(m - mx) : 1.f;
+#pragma unroll
+          for (int c = 0; c < DH / 32; c++) {
+            pw_ld32(tO + 32 * c, s);
+            pw_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[e] = __float_as_uint(__uint_as_float(s[e]) * corr);
+            pw_st32(tO + 32 * c, s);
+          }
+          pw_wait_st();
+          l *= corr;
+        }
+        if (grow) m = mx;
+        const float base = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(A.scale_log2, A.scale_log2), nb2 = make_float2(-base, -base);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          pw_ld32(tS + 32 * c, s);
+          pw_wait_ld();
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            x = ffma2(x, sc2, nb2);
+            x.x = pa_exp2(x.x);
+            x.y = pa_exp2(x.y);
+            sum = fadd2(sum, x);
+            p[e] = pack_bf16(x.x, x.y);
+          }
+          pw_st16(tS + 16 * c, p);
+        }
+        l += sum.x + sum.y;
+        pw_wait_st();
+        tc_fence_before();
+        tc_mbar_arrive(p_full + t);
+      }
+      if (!ok) break;
+      if (I.nk > 0 && !pw_wait(o_full + t, (n_t + I.nk - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      n_tile += I.nk;
+      n_t += I.nk;
+      const bool on = r < I.R;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float *part = A.part + ((size_t)parts[I.b] + ((size_t)tok * A.heads + head) * I.S.splits +
+                              I.split) * (DH + 2);
+      bf16 *dst = static_cast<bf16 *>(A.out) + (int64_t)(I.row0 + tok) * A.ldo + head * DH;
+#pragma unroll
+      for (int c = 0; c < DH / 32; c++) {
+        uint32_t s[32];
+        if (I.nk > 0) {
+          pw_ld32(tO + 32 * c, s);
+          pw_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e++) s[e] = 0;
+        }
+        if (!on) continue;
+        if (I.S.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            *reinterpret_cast<float2 *>(part + 32 * c + e) =
+                make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; y++)
+              w[y] = pack_bf16(__uint_as_float(s[e + 2 * y]) * inv,
+                               __uint_as_float(s[e + 2 * y + 1]) * inv);
+            *reinterpret_cast<uint4 *>(dst + 32 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (on) {
+        if (I.S.splits > 1)
+          *reinterpret_cast<float2 *>(part + DH) = make_float2(m, l);
+        else if (A.lse)
+          A.lse[(size_t)(I.row0 + tok) * A.heads + head] = (m + log2f(l)) * 0.69314718055994531f;
+      }
+      // O is read before the next item's first P lets it be written
+      tc_fence_before();
+    }
+    if (!ok) *fail = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && s_fail) flag_rows(A.R, RLT_PAGED_TIMEOUT);
+  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (A.follows) pdl_wait();
+}
+
+}  // namespace rlt

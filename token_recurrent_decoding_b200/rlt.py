@@ -80,7 +80,7 @@ class rlt_paged_rows(C.Structure):
 
 
 KV_PLAIN, KV_E4M3 = 0, 1
-PAGED_BAD_PAGE, PAGED_BAD_ROWS = 1, 2
+PAGED_BAD_PAGE, PAGED_BAD_ROWS, PAGED_TIMEOUT = 1, 2, 4
 
 
 class rlt_stats(C.Structure):
