@@ -234,9 +234,16 @@ __device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// 2^x on the special-function unit; results below 2^-126 are zeros, which
+// weights relative to a maximum of one may be.
 __device__ __forceinline__ float pa_exp2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 

@@ -9,7 +9,7 @@
 //   warps 8-11      loaders: queries, keys, values into shared memory in the
 //                   128-byte swizzle the MMA reads; bf16 rows with cp.async,
 //                   8-bit rows through registers as bf16 values
-//   warp 12         one lane issues tcgen05.mma
+//   warp 12         one lane issues tcgen05.mma (warps 13-15 only give up registers)
 // S_t = Q_t K^T goes to tensor memory (128 x 128 fp32); the softmax writes P
 // over it as bf16 (packed two keys a column), and O_t += P_t V takes P from
 // tensor memory and V as an MN-major operand as it lies in the cache. The
@@ -36,7 +36,10 @@
 
 namespace rlt {
 
-constexpr int PW_THREADS = 416, PW_LOADERS = 128;
+constexpr int PW_THREADS = 512, PW_LOADERS = 128;
+// Registers of a thread of the softmax, loader and MMA warpgroups: 2 * 184 + 88
+// + 56 = 4 * 128, what the block is launched with.
+constexpr int PW_REGS_SOFTMAX = 184, PW_REGS_LOADER = 88, PW_REGS_MMA = 56;
 constexpr int PW_TK = 128;                // keys of a tile
 constexpr int PW_RT = 256;                // query rows of an item
 
@@ -56,11 +59,15 @@ template <int DH> struct PwCfg {
   static int bytes(int n) { return PLAN + 2 * (n + 1) * 4 + 1024; }
 };
 
+// Warp-uniform bounded wait: the warp leaves together (what follows is often
+// warp-collective). The clock is read only once the first polls have failed.
 __device__ __forceinline__ bool pw_wait(uint64_t *bar, unsigned parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; i++)
+    if (__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    const bool done = mbar_test_wait(bar, parity);
-    if (__all_sync(FULL_MASK, done)) return true;
+    if (__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) return true;
     if (__shfl_sync(FULL_MASK, globaltimer_ns() - t0 > WAIT_LIMIT_NS_TC, 0)) return false;
   }
 }
@@ -98,17 +105,6 @@ __device__ __forceinline__ void pw_ld32(uint32_t taddr, uint32_t r[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void pw_st32(uint32_t taddr, const uint32_t r[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void pw_st16(uint32_t taddr, const uint32_t r[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -125,6 +121,17 @@ __device__ __forceinline__ void pw_wait_st() {
 }
 __device__ __forceinline__ void pw_fence_async() {
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+// An arrival once this thread's cp.async copies so far are complete.
+__device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
+               : "memory");
+}
+template <int N> __device__ __forceinline__ void reg_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 // Two fp32 multiply-adds, two additions.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     for (int i = 0; i < ST; i++) {
       mbar_init(k_full + i, PW_LOADERS);
       mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, PW_LOADERS);
+      mbar_init(v_full + i, PW_LOADERS + 1);  // and the flags' writer
       mbar_init(v_empty + i, 1);
     }
     for (int t = 0; t < 2; t++) {
@@ -233,6 +240,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
 
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------- loaders
+    reg_shrink<PW_REGS_LOADER>();
     const int tid = threadIdx.x - 256;
     uint32_t n_item = 0, n_tile = 0;  // items and key tiles so far (barrier phases)
     bool ok = true;
@@ -259,67 +267,89 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
                             pw_piece(r & 127, c & 7)),
                    src, r < I.R ? 16 : 0);
       }
-      cp_async_commit();
+      arrive_behind_copies(q_full);
 
-      // pages of a key tile: lane j < 8 holds that of keys 16 j .. 16 j + 15
+      // pages of a key tile: lane j < 8 holds the row of the cache's key plane
+      // where keys 16 j .. 16 j + 15 begin (rows of 64 bytes and more: 32 bits
+      // reach over any GPU's memory), or NO_PAGE
+      constexpr uint32_t NO_PAGE = 0xffffffffu;
       auto pages_of = [&](int i) {
-        int pid = -1;
+        uint32_t cell = NO_PAGE;
         const int key = I.k0 + i * PW_TK + (lane & 7) * PA_TK;
         if (lane < 8 && key < I.k1) {
           const int idx = key / A.C.P;
+          int pid = -1;
           if (idx < A.R.width) pid = A.R.table[(size_t)I.b * A.R.width + idx];
-          if (pid < 0 || pid >= A.C.n_pages) {
-            pid = -1;
+          if (pid >= 0 && pid < A.C.n_pages)
+            cell = ((uint32_t)pid * A.C.H + I.kvh) * 2u * A.C.P + (key - idx * A.C.P);
+          else
             flag_rows(A.R, RLT_PAGED_BAD_PAGE);
-          }
         }
-        return pid;
-      };
-      // row (of positions) of the cache's key plane that holds key (page pid >= 0)
-      auto cell_of = [&](int pid, int key) {
-        return ((size_t)pid * A.C.H + I.kvh) * 2 * A.C.P + key % A.C.P;
+        return cell;
       };
       // flags of tile i: keys that do not exist, keys whose values were cleared
       auto flag_word = [&](int i, int w) -> uint32_t * {
         return flags + ((n_tile + i) % Cfg::INFO) * 8 + w;
       };
 
+      // by threads 0 .. 3: two groups of 16 keys a word
+      auto write_flags = [&](int i, uint32_t gone) {
+        const uint32_t g2 = gone >> (2 * tid);
+        *flag_word(i, tid) = ((g2 & 1) ? 0xffffu : 0u) | ((g2 & 2) ? 0xffff0000u : 0u);
+        *flag_word(i, 4 + tid) = 0;
+      };
+
       if constexpr (!E4) {
-        // unit 0: Q; 1 + 2 i: K of tile i; 2 + 2 i: V of tile i. A unit is one
-        // cp.async group; it is handed on two units later, or at once when the
-        // loader would block on a stage that is still read.
         constexpr int PASSES = DH / 8;             // 128 * DH / 8 pieces by 128 threads
         constexpr int RPP = 128 / (DH / 8);        // rows of a pass: 8 or 16
-        int issued = 1, handed = 0;
-        uint64_t absent = 0;  // 8 bits a tile: 16-key groups without a page
-        auto hand = [&]() {
-          const int u = handed++;
-          if (u == 0) {
-            pw_fence_async();
-            tc_mbar_arrive(q_full);
-            return;
-          }
-          const int i = (u - 1) >> 1, st = (n_tile + i) % ST;
-          if (u & 1) {
-            pw_fence_async();
-            tc_mbar_arrive(k_full + st);
-            return;
-          }
+        uint32_t cells = pages_of(0);
+        const int c = tid % (DH / 8), row_in = tid / (DH / 8);
+        const bf16 *thread_src = reinterpret_cast<const bf16 *>(A.C.pages) +
+                                 (size_t)(row_in % PA_TK) * DH + c * 8;
+        const uint32_t thread_dst = (c >> 3) * Cfg::HALF + pw_piece(row_in, c & 7);
+        for (int i = 0; ok && i < I.nk; i++) {
+          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
           const int key0 = I.k0 + i * PW_TK;
-          const uint32_t gone = (uint32_t)(absent >> (8 * (i & 7))) & 0xffu;
-          if (gone || !pw_all_see(A, I, key0, pos_lo, pos_hi)) {
-            if (tid < 4) {
-              // two groups of 16 keys a word
-              const uint32_t g2 = gone >> (2 * tid);
-              *flag_word(i, tid) = ((g2 & 1) ? 0xffffu : 0u) | ((g2 & 2) ? 0xffff0000u : 0u);
-              *flag_word(i, 4 + tid) = 0;
+          const uint32_t next = i + 1 < I.nk ? pages_of(i + 1) : NO_PAGE;
+          const unsigned gone = __ballot_sync(FULL_MASK, lane < 8 && cells == NO_PAGE &&
+                                                             key0 + lane * PA_TK < I.k1) & 0xffu;
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++) {
+            uint64_t *empty = (kv ? v_empty : k_empty) + st;
+            if (use > 0 && !pw_wait(empty, (use - 1) & 1)) {
+              ok = false;
+              break;
             }
+            const uint32_t dst =
+                smem_u32(sm + (kv ? Cfg::V : Cfg::K) + st * Cfg::TILE) + thread_dst;
+            const size_t plane = kv ? (size_t)A.C.P * DH : 0;
+#pragma unroll
+            for (int p = 0; p < PASSES; p++) {
+              const uint32_t cell = __shfl_sync(FULL_MASK, cells, p * RPP / PA_TK);
+              const bool on = cell != NO_PAGE && key0 + p * RPP + row_in < I.S.k_hi;
+              const bf16 *src = thread_src + plane;
+              if (on) src += (size_t)(cell + p * RPP % PA_TK) * DH;
+              cp_async16(dst + p * RPP * 128, src, on ? 16 : 0);
+            }
+            if (kv == 0 || (!gone && pw_all_see(A, I, key0, pos_lo, pos_hi))) {
+              // handed on when the copies land; the tensor core's side fences
+              if (kv == 1 && tid == 0) {
+                for (int w = 0; w < 8; w++) *flag_word(i, w) = 0;
+                tc_mbar_arrive(v_full + st);
+              }
+              arrive_behind_copies((kv ? v_full : k_full) + st);
+              continue;
+            }
+            // values that some row does not see
+            cp_async_commit();
+            cp_async_wait<0>();
+            if (tid < 4) write_flags(i, gone);
             asm volatile("bar.sync 1, 128;\n" ::: "memory");
 #pragma unroll 1
             for (int p = 0; p < PASSES; p++) {
-              const int row = p * RPP + tid / (DH / 8), c = tid % (DH / 8);
-              uint4 *v = reinterpret_cast<uint4 *>(sm + Cfg::V + st * Cfg::TILE +
-                                                   (c >> 3) * Cfg::HALF + pw_piece(row, c & 7));
+              const int row = p * RPP + row_in;
+              uint4 *v = reinterpret_cast<uint4 *>(sm + Cfg::V + st * Cfg::TILE + thread_dst +
+                                                   p * RPP * 128);
               const uint4 x = *v;
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               bool bad = false;
@@ -331,59 +361,13 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
                 atomicOr(flag_word(i, 4 + (row >> 5)), 1u << (row & 31));
               }
             }
-          } else if (tid < 8) {
-            *flag_word(i, tid) = 0;
+            pw_fence_async();
+            tc_mbar_arrive(v_full + st);
+            if (tid == 0) tc_mbar_arrive(v_full + st);
           }
-          pw_fence_async();
-          tc_mbar_arrive(v_full + st);
-        };
-        auto hand_all = [&]() {
-          cp_async_wait<0>();
-          while (handed < issued) hand();
-        };
-        int pid = pages_of(0);
-        for (int i = 0; ok && i < I.nk; i++) {
-          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
-          const int key0 = I.k0 + i * PW_TK;
-          const int pid_next = i + 1 < I.nk ? pages_of(i + 1) : -1;
-          const unsigned gone =
-              __ballot_sync(FULL_MASK, lane < 8 && pid < 0 && key0 + lane * PA_TK < I.k1) & 0xffu;
-          absent = (absent & ~((uint64_t)0xff << (8 * (i & 7)))) | (uint64_t)gone << (8 * (i & 7));
-#pragma unroll
-          for (int kv = 0; kv < 2; kv++) {
-            uint64_t *empty = (kv ? v_empty : k_empty) + st;
-            if (use > 0) {
-              if (!__all_sync(FULL_MASK, mbar_test_wait(empty, (use - 1) & 1))) hand_all();
-              if (!pw_wait(empty, (use - 1) & 1)) {
-                ok = false;
-                break;
-              }
-            }
-            const uint32_t dst = smem_u32(sm + (kv ? Cfg::V : Cfg::K) + st * Cfg::TILE);
-            const int c = tid % (DH / 8);
-#pragma unroll 8
-            for (int p = 0; p < PASSES; p++) {
-              const int row = p * RPP + tid / (DH / 8), key = key0 + row;
-              const int pg = __shfl_sync(FULL_MASK, pid, p * RPP / PA_TK);
-              const bool on = pg >= 0 && key < I.S.k_hi;
-              const bf16 *src = reinterpret_cast<const bf16 *>(A.C.pages) +
-                                (on ? (cell_of(pg, key) + (kv ? A.C.P : 0)) * DH + c * 8 : 0);
-              cp_async16(dst + (c >> 3) * Cfg::HALF + pw_piece(row, c & 7), src, on ? 16 : 0);
-            }
-            cp_async_commit();
-            issued++;
-            if (issued - handed > 2) {
-              cp_async_wait<2>();
-              hand();
-            }
-          }
-          pid = pid_next;
+          cells = next;
         }
-        hand_all();
       } else {
-        cp_async_wait<0>();
-        pw_fence_async();
-        tc_mbar_arrive(q_full);
         // codes through registers: the next unit's are fetched before this
         // thread waits for its stage
         constexpr int CPR = DH / 16;               // pieces of 16 codes of a row
@@ -393,21 +377,20 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         uint4 code[PASSES];
         uint32_t sbyte[PASSES];
         const int c = tid % CPR, row_in = tid / CPR;
-        int pid = -1;
-        uint32_t gone = 0;
+        uint32_t cells = NO_PAGE, gone = 0;
         auto fetch = [&](int i, int kv) {
           const int key0 = I.k0 + i * PW_TK;
           if (kv == 0) {
-            pid = pages_of(i);
-            gone = __ballot_sync(FULL_MASK, lane < 8 && pid < 0 && key0 + lane * PA_TK < I.k1) &
-                   0xffu;
+            cells = pages_of(i);
+            gone = __ballot_sync(FULL_MASK, lane < 8 && cells == NO_PAGE &&
+                                                key0 + lane * PA_TK < I.k1) & 0xffu;
           }
 #pragma unroll
           for (int p = 0; p < PASSES; p++) {
-            const int row = p * RPP + row_in, key = key0 + row;
-            const int pg = __shfl_sync(FULL_MASK, pid, row / PA_TK);
-            const bool on = pg >= 0 && key < I.S.k_hi;
-            const size_t cell = on ? cell_of(pg, key) + (kv ? A.C.P : 0) : 0;
+            const int row = p * RPP + row_in;
+            const uint32_t first = __shfl_sync(FULL_MASK, cells, row / PA_TK);
+            const bool on = first != NO_PAGE && key0 + row < I.S.k_hi;
+            const size_t cell = (size_t)first + row % PA_TK + (kv ? A.C.P : 0);
             code[p] = make_uint4(0, 0, 0, 0);
             sbyte[p] = 127;
             if (on) {
@@ -428,14 +411,10 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
             }
             const bool masked = kv == 1 && (gone || !pw_all_see(A, I, key0, pos_lo, pos_hi));
             if (masked) {
-              if (tid < 4) {
-                const uint32_t g2 = gone >> (2 * tid);
-                *flag_word(i, tid) = ((g2 & 1) ? 0xffffu : 0u) | ((g2 & 2) ? 0xffff0000u : 0u);
-                *flag_word(i, 4 + tid) = 0;
-              }
+              if (tid < 4) write_flags(i, gone);
               asm volatile("bar.sync 1, 128;\n" ::: "memory");
-            } else if (kv == 1 && tid < 8) {
-              *flag_word(i, tid) = 0;
+            } else if (kv == 1 && tid == 0) {
+              for (int w = 0; w < 8; w++) *flag_word(i, w) = 0;
             }
             uint8_t *dst = sm + (kv ? Cfg::V : Cfg::K) + st * Cfg::TILE + (c >> 2) * Cfg::HALF;
 #pragma unroll
@@ -462,6 +441,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
             }
             pw_fence_async();
             tc_mbar_arrive((kv ? v_full : k_full) + st);
+            if (kv == 1 && tid == 0) tc_mbar_arrive(v_full + st);
             if (kv == 0)
               fetch(i, 1);
             else if (i + 1 < I.nk)
@@ -472,16 +452,20 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       n_item++;
       n_tile += I.nk;
     }
+    cp_async_commit();
+    cp_async_wait<0>();  // after a wait that gave up copies may be in flight
     if (!ok) *fail = 1;
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    reg_shrink<PW_REGS_MMA>();
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t idS = idesc_bf16_f32(128, PW_TK);
       constexpr uint32_t idO = idesc_bf16_f32(128, DH) | (1u << 16);  // V: MN-major
       uint32_t n_item = 0, n_tile = 0, n_t[2] = {0, 0};
       bool ok = true;
       auto wait = [&](uint64_t *bar, unsigned parity) {
         if (ok && !mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS_TC)) ok = false;
+        pw_fence_async();  // copies of other threads that the barrier counted -> the tensor core
         tc_fence_after();
         return ok;
       };
@@ -532,6 +516,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
+    reg_grow<PW_REGS_SOFTMAX>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = tmem + 256 + t * DH + ((uint32_t)((warp & 3) * 32) << 16);
@@ -561,38 +546,31 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
         const bool all = pw_all_see(A, I, key0, pos_lo, pos_hi) &&
                          !(fl[0] | fl[1] | fl[2] | fl[3]);
-        // the row's maximum
-        float mx = -INFINITY;
-        uint32_t s[32];
-        if (all) {
+        // the row of scores and its maximum
+        uint32_t s[128];
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            pw_ld32(tS + 32 * c, s);
-            pw_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e++) mx = fmaxf(mx, __uint_as_float(s[e]));
-          }
-        } else {
+        for (int c = 0; c < 4; c++) pw_ld32(tS + 32 * c, s + 32 * c);
+        pw_wait_ld();
+        if (!all) {
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             // keys of the chunk the row sees, as bits
             const int k0 = key0 + 32 * c;
-            const int hi = min(min(pos, I.k1 - 1) - k0, 31);                // last seen
+            const int hi = min(min(pos, I.k1 - 1) - k0, 31);                    // last seen
             const int lo = A.window > 0 ? max(pos - A.window + 1 - k0, 0) : 0;  // first seen
             uint32_t see = hi < 0 || lo > 31 ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
             see &= ~fl[c];
             if (see & fl[4 + c]) l = NAN;
-            pw_ld32(tS + 32 * c, s);
-            pw_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e++) {
-              if (!(see >> e & 1)) s[e] = 0xff800000u;
-              mx = fmaxf(mx, __uint_as_float(s[e]));
-            }
-            pw_st32(tS + 32 * c, s);
+            for (int e = 0; e < 32; e++)
+              if (!(see >> e & 1)) s[32 * c + e] = 0xff800000u;
           }
-          pw_wait_st();
         }
+        float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 2)
+          mxs[(e >> 1) & 3] = max3(mxs[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
         mx *= A.scale_log2;
         // O keeps its reference until the maximum has outgrown it by 2^8
         const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
@@ -603,13 +581,14 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
           }
           tc_fence_after();
           const float corr = grow ? pa_exp2(m - mx) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < DH / 16; c++) {
+            float v[16];
+            tmem_ld16(tO + 16 * c, v);
+            uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < DH / 32; c++) {
-            pw_ld32(tO + 32 * c, s);
-            pw_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e++) s[e] = __float_as_uint(__uint_as_float(s[e]) * corr);
-            pw_st32(tO + 32 * c, s);
+            for (int e = 0; e < 16; e++) w[e] = __float_as_uint(v[e] * corr);
+            pw_st16(tO + 16 * c, w);
           }
           pw_wait_st();
           l *= corr;
@@ -620,12 +599,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          pw_ld32(tS + 32 * c, s);
-          pw_wait_ld();
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            float2 x = make_float2(__uint_as_float(s[32 * c + 2 * e]),
+                                   __uint_as_float(s[32 * c + 2 * e + 1]));
             x = ffma2(x, sc2, nb2);
             x.x = pa_exp2(x.x);
             x.y = pa_exp2(x.y);
