@@ -66,7 +66,8 @@ __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_head
   s.k_lo = min(lo, s.k_hi) & ~(PA_TK - 1);
   const int span = s.k_hi - s.k_lo;
   const int units = max(1, kv_heads * ceil_div(m * group, wide ? PA_WIDE_ROWS : PA_UNIT_ROWS));
-  int n = min(min(PA_MAX_SPLITS, ceil_div(wide ? PA_WIDE_UNITS : PA_SPLIT_UNITS, units)),
+  // (a wide unit fills an SM: rounded down, two thirds of a second wave cost more than idle SMs)
+  int n = min(min(PA_MAX_SPLITS, wide ? PA_WIDE_UNITS / units : ceil_div(PA_SPLIT_UNITS, units)),
               ceil_div(span, wide ? PA_WIDE_KEYS : PA_MIN_KEYS));
   n = max(n, 1);
   s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);

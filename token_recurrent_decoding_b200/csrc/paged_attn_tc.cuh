@@ -9,12 +9,13 @@
 //   warps 8-11      loaders: queries, keys, values into shared memory in the
 //                   128-byte swizzle the MMA reads; bf16 rows with cp.async,
 //                   8-bit rows through registers as bf16 values
-//   warp 12         one lane issues tcgen05.mma (warps 13-15 only give up registers)
+//   warps 12, 13    issue the tcgen05.mma of row tile 0, 1
+//   warp 14         one lane relays loaded stages (warp 15 only gives up registers)
 // S_t = Q_t K^T goes to tensor memory (128 x 128 fp32); the softmax writes P
 // over it as bf16 (packed two keys a column), and O_t += P_t V takes P from
-// tensor memory and V as an MN-major operand as it lies in the cache. The
-// issue order PV_0(i), S_0(i+1), PV_1(i), S_1(i+1) lets one tile's softmax run
-// under the other tile's products.
+// tensor memory and V as an MN-major operand as it lies in the cache. Each
+// tile is a chain S(i), softmax, PV(i), S(i+1); the two chains run side by
+// side, one tile's softmax under the other's products.
 //
 // Softmax: O is rescaled (in tensor memory, by the softmax warps) only when a
 // row's maximum has grown by more than 2^8 since the reference it is scaled
@@ -52,7 +53,7 @@ template <int DH> struct PwCfg {
   static constexpr int K = 2 * TILE;
   static constexpr int V = K + STAGES * TILE;
   static constexpr int BARS = V + STAGES * TILE;
-  static constexpr int NBARS = 2 + 4 * STAGES + 6;
+  static constexpr int NBARS = 3 + 6 * STAGES + 8;
   static constexpr int FLAGS = BARS + NBARS * 8;   // [INFO][8] words: unseen keys, strange keys
   static constexpr int SLOT = FLAGS + INFO * 8 * 4;
   static constexpr int PLAN = SLOT + 16;
@@ -105,6 +106,17 @@ __device__ __forceinline__ void pw_ld32(uint32_t taddr, uint32_t r[32]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void pw_st32(uint32_t taddr, const uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void pw_st16(uint32_t taddr, const uint32_t r[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -126,6 +138,13 @@ __device__ __forceinline__ void pw_fence_async() {
 __device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
                : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(one));
+  return one != 0;
 }
 template <int N> __device__ __forceinline__ void reg_shrink() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -198,9 +217,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   uint8_t *sm = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(pw_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::BARS);
-  uint64_t *q_full = bars, *q_empty = bars + 1, *k_full = bars + 2, *k_empty = k_full + ST,
-           *v_full = k_empty + ST, *v_empty = v_full + ST, *s_full = v_empty + ST,
-           *p_full = s_full + 2, *o_full = p_full + 2;
+  // *_in: counted by the loaders; *_full: passed on by the relay
+  uint64_t *q_in = bars, *q_full = bars + 1, *q_empty = bars + 2, *k_in = bars + 3,
+           *k_full = k_in + ST, *k_empty = k_full + ST, *v_in = k_empty + ST, *v_full = v_in + ST,
+           *v_empty = v_full + ST, *s_full = v_empty + ST, *p_full = s_full + 2,
+           *o_full = p_full + 4;  // p_full[t][part of the keys]
   uint32_t *flags = reinterpret_cast<uint32_t *>(sm + Cfg::FLAGS);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Cfg::SLOT);
   int *items = reinterpret_cast<int *>(sm + Cfg::PLAN), *parts = items + A.R.n + 1;
@@ -209,17 +230,21 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
 
   if (threadIdx.x == 0) {
     s_fail = 0;
-    mbar_init(q_full, PW_LOADERS);
-    mbar_init(q_empty, 1);
+    mbar_init(q_in, PW_LOADERS);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);  // one for each row tile
     for (int i = 0; i < ST; i++) {
-      mbar_init(k_full + i, PW_LOADERS);
-      mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, PW_LOADERS + 1);  // and the flags' writer
-      mbar_init(v_empty + i, 1);
+      mbar_init(k_in + i, PW_LOADERS);
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 2);
+      mbar_init(v_in + i, PW_LOADERS + 1);  // and the flags' writer
+      mbar_init(v_full + i, 1);
+      mbar_init(v_empty + i, 2);
     }
     for (int t = 0; t < 2; t++) {
       mbar_init(s_full + t, 1);
-      mbar_init(p_full + t, 128);
+      mbar_init(p_full + 2 * t, 128);
+      mbar_init(p_full + 2 * t + 1, 128);
       mbar_init(o_full + t, 1);
     }
     fence_mbar_init();
@@ -267,7 +292,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
                             pw_piece(r & 127, c & 7)),
                    src, r < I.R ? 16 : 0);
       }
-      arrive_behind_copies(q_full);
+      arrive_behind_copies(q_in);
 
       // pages of a key tile: lane j < 8 holds the row of the cache's key plane
       // where keys 16 j .. 16 j + 15 begin (rows of 64 bytes and more: 32 bits
@@ -332,12 +357,12 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
               cp_async16(dst + p * RPP * 128, src, on ? 16 : 0);
             }
             if (kv == 0 || (!gone && pw_all_see(A, I, key0, pos_lo, pos_hi))) {
-              // handed on when the copies land; the tensor core's side fences
+              // counted when the copies land
               if (kv == 1 && tid == 0) {
                 for (int w = 0; w < 8; w++) *flag_word(i, w) = 0;
-                tc_mbar_arrive(v_full + st);
+                tc_mbar_arrive(v_in + st);
               }
-              arrive_behind_copies((kv ? v_full : k_full) + st);
+              arrive_behind_copies((kv ? v_in : k_in) + st);
               continue;
             }
             // values that some row does not see
@@ -361,9 +386,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
                 atomicOr(flag_word(i, 4 + (row >> 5)), 1u << (row & 31));
               }
             }
-            pw_fence_async();
-            tc_mbar_arrive(v_full + st);
-            if (tid == 0) tc_mbar_arrive(v_full + st);
+            tc_mbar_arrive(v_in + st);
+            if (tid == 0) tc_mbar_arrive(v_in + st);
           }
           cells = next;
         }
@@ -439,9 +463,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
               *reinterpret_cast<uint4 *>(dst + pw_piece(row, c8 + 1)) =
                   make_uint4(o[4], o[5], o[6], o[7]);
             }
-            pw_fence_async();
-            tc_mbar_arrive((kv ? v_full : k_full) + st);
-            if (kv == 1 && tid == 0) tc_mbar_arrive(v_full + st);
+            tc_mbar_arrive((kv ? v_in : k_in) + st);
+            if (kv == 1 && tid == 0) tc_mbar_arrive(v_in + st);
             if (kv == 0)
               fetch(i, 1);
             else if (i + 1 < I.nk)
@@ -458,58 +481,102 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   } else if (warp >= 12) {
     // ---------------------------------------------------------- MMA issuer
     reg_shrink<PW_REGS_MMA>();
-    if (warp == 12 && lane == 0) {
+    if (warp <= 13) {
+      // One warp per row tile; the whole warp walks the loop, so that
+      // descriptors stay uniform, and one elected lane issues.
       constexpr uint32_t idS = idesc_bf16_f32(128, PW_TK);
       constexpr uint32_t idO = idesc_bf16_f32(128, DH) | (1u << 16);  // V: MN-major
-      uint32_t n_item = 0, n_tile = 0, n_t[2] = {0, 0};
+      const int t = warp - 12;
+      const uint64_t q0 = smem_desc_sw128(sm + Cfg::Q + t * Cfg::TILE);
+      const uint64_t k0 = smem_desc_sw128(sm + Cfg::K);
+      const uint64_t v0 = pw_desc_v(smem_u32(sm + Cfg::V), Cfg::HALF);
+      const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * DH;
+      uint32_t n_item = 0, n_tile = 0, n_t = 0;
       bool ok = true;
-      auto wait = [&](uint64_t *bar, unsigned parity) {
-        if (ok && !mbar_wait_bounded(bar, parity, WAIT_LIMIT_NS_TC)) ok = false;
-        pw_fence_async();  // copies of other threads that the barrier counted -> the tensor core
-        tc_fence_after();
-        return ok;
-      };
-      auto scores = [&](int t, int i) {
-        const uint64_t qd = smem_desc_sw128(sm + Cfg::Q + t * Cfg::TILE);
-        const uint64_t kd = smem_desc_sw128(sm + Cfg::K + ((n_tile + i) % ST) * Cfg::TILE);
+      auto scores = [&](int i) {
+        const uint64_t kd = k0 + (uint64_t)(((n_tile + i) % ST) * (Cfg::TILE >> 4));
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < DH / 16; k++) {
-          const uint64_t at = (uint64_t)(k >> 2) * (Cfg::HALF >> 4) + 2 * (k & 3);
-          umma_bf16(tmem + t * 128, qd + at, kd + at, idS, k > 0 ? 1u : 0u);
+          for (int k = 0; k < DH / 16; k++) {
+            const uint64_t at = (uint64_t)((k >> 2) * (Cfg::HALF >> 4) + 2 * (k & 3));
+            umma_bf16(tS, q0 + at, kd + at, idS, k > 0 ? 1u : 0u);
+          }
+          umma_commit(s_full + t);
         }
-        umma_commit(s_full + t);
+        __syncwarp();
       };
       for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
         PwItem I;
         if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
-        const int nt = I.R > 128 ? 2 : 1;
-        if (!wait(q_full, n_item & 1)) break;
-        for (int i = 0; ok && i <= I.nk; i++) {
-          // PV of tile i - 1 and the scores of tile i, row tile by row tile
-          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
-          const int pst = (n_tile + i + ST - 1) % ST, puse = (n_tile + i - 1) / ST;
-          if (i < I.nk && !wait(k_full + st, use & 1)) break;
-          if (i > 0 && !wait(v_full + pst, puse & 1)) break;
-          for (int t = 0; t < nt; t++) {
-            if (i > 0) {
-              if (!wait(p_full + t, (n_t[t] + i - 1) & 1)) break;
-              const uint32_t v0 = smem_u32(sm + Cfg::V + pst * Cfg::TILE);
-#pragma unroll
-              for (int k = 0; k < PW_TK / 16; k++)
-                umma_ts(tmem + 256 + t * DH, tmem + t * 128 + k * 8,
-                        pw_desc_v(v0 + k * 2048, Cfg::HALF), idO, (i > 1 || k > 0) ? 1u : 0u);
-              umma_commit(o_full + t);
-            }
-            if (i < I.nk) scores(t, i);
-          }
+        // Every item's queries are waited for, an idle tile's too, and the second
+        // arrival on q_empty comes from here where the tile is idle: a warp
+        // that the phases overtook would take an old phase for the next.
+        ok = pw_wait(q_full, n_item & 1);
+        if (!ok) break;
+        if (t == 1 && I.R <= 128) {
+          if (lane == 0) tc_mbar_arrive(q_empty);
+        } else {
+          ok = pw_wait(k_full + n_tile % ST, n_tile / ST & 1);
           if (!ok) break;
-          if (i < I.nk) umma_commit(k_empty + st);
-          if (i > 0) umma_commit(v_empty + pst);
-          if (i + 1 == I.nk) umma_commit(q_empty);
+          tc_fence_after();
+          scores(0);
+          for (int i = 0; i < I.nk; i++) {
+            // PV of tile i in two parts as P comes, then the scores of tile i + 1.
+            // The softmax has waited for V before it hands P on.
+            const uint64_t vd = v0 + (uint64_t)(((n_tile + i) % ST) * (Cfg::TILE >> 4));
+            const bool more = i + 1 < I.nk;
+            if (more) ok = pw_wait(k_full + (n_tile + i + 1) % ST, (n_tile + i + 1) / ST & 1);
+            ok = ok && pw_wait(p_full + 2 * t, (n_t + i) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 6; k++)
+                umma_ts(tO, tS + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO,
+                        (i > 0 || k > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            ok = pw_wait(p_full + 2 * t + 1, (n_t + i) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 6; k < 8; k++)
+                umma_ts(tO, tS + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO, 1u);
+              if (!more) umma_commit(o_full + t);
+            }
+            __syncwarp();
+            if (more) scores(i + 1);
+          }
+          n_t += I.nk;
         }
         n_item++;
         n_tile += I.nk;
-        for (int t = 0; t < nt; t++) n_t[t] += I.nk;
+      }
+      if (!ok) *fail = 1;
+    }
+    if (warp == 14 && lane == 0) {
+      // The relay: what the loaders wrote (through the generic proxy, some of it
+      // by asynchronous copies that only the barrier knows of) is fenced for the
+      // tensor core here, so that the issuing thread does not spend the fence.
+      uint32_t n_item = 0, n_tile = 0;
+      bool ok = true;
+      auto pass_on = [&](uint64_t *in, uint64_t *full, unsigned parity) {
+        if (ok && !mbar_wait_bounded(in, parity, WAIT_LIMIT_NS_TC)) ok = false;
+        pw_fence_async();
+        if (ok) tc_mbar_arrive(full);
+      };
+      for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
+        PwItem I;
+        if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
+        pass_on(q_in, q_full, n_item & 1);
+        for (int i = 0; ok && i < I.nk; i++) {
+          const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
+          pass_on(k_in + st, k_full + st, use & 1);
+          pass_on(v_in + st, v_full + st, use & 1);
+        }
+        n_item++;
+        n_tile += I.nk;
       }
       if (!ok) *fail = 1;
     }
@@ -520,11 +587,20 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = tmem + 256 + t * DH + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t n_tile = 0, n_t = 0;
+    uint32_t n_tile = 0, n_t = 0, n_item = 0;
     bool ok = true;
     for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
       PwItem I;
       if (!pw_item(A, items, parts, it, I)) continue;
+      // Products complete in the order of their issue: once the scores of tile i
+      // are there, K of tile i, V and P of tile i - 1 have been read. One thread
+      // of each row tile gives stages back (of the only one twice).
+      auto give_back = [&](uint64_t *empty) {
+        if (row == 0) {
+          tc_mbar_arrive(empty);
+          if (I.R <= 128) tc_mbar_arrive(empty);
+        }
+      };
       const int r = t * 128 + row;  // row of the item
       const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
       const int pos = r < I.R ? I.S.first + tok : -1;
@@ -538,11 +614,14 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       for (int i = 0; i < I.nk; i++) {
         const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
         const int key0 = I.k0 + i * PW_TK;
-        if (!pw_wait(v_full + st, use & 1) || !pw_wait(s_full + t, (n_t + i) & 1)) {
+        // (in this order: V's phase is known to be this tile's once the scores are)
+        if (!pw_wait(s_full + t, (n_t + i) & 1) || !pw_wait(v_full + st, use & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        give_back(k_empty + st);
+        if (i > 0) give_back(v_empty + (n_tile + i - 1) % ST);
         const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
         const bool all = pw_all_see(A, I, key0, pos_lo, pos_hi) &&
                          !(fl[0] | fl[1] | fl[2] | fl[3]);
@@ -575,11 +654,6 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         // O keeps its reference until the maximum has outgrown it by 2^8
         const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
         if (i > 0 && __any_sync(FULL_MASK, grow)) {
-          if (!pw_wait(o_full + t, (n_t + i - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
           const float corr = grow ? pa_exp2(m - mx) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < DH / 16; c++) {
@@ -596,33 +670,50 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         if (grow) m = mx;
         const float base = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(A.scale_log2, A.scale_log2), nb2 = make_float2(-base, -base);
-        float2 sum = make_float2(0.f, 0.f);
+        // weights, packed in place: pair e of keys becomes s[e]. P is handed on
+        // in two parts, 96 keys and 32, so that most of PV runs under the last
+        // exponentials; stores are waited for a few pairs after their issue.
+        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weigh = [&](int e) {
+          float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+          x = ffma2(x, sc2, nb2);
+          x.x = pa_exp2(x.x);
+          x.y = pa_exp2(x.y);
+          sums[e & 1] = fadd2(sums[e & 1], x);
+          s[e] = pack_bf16(x.x, x.y);
+        };
+        auto hand_on = [&](int part) {
+          pw_wait_st();
+          tc_fence_before();
+          tc_mbar_arrive(p_full + 2 * t + part);
+        };
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          uint32_t p[16];
+        for (int e = 0; e < 32; e++) weigh(e);
+        pw_st32(tS, s);
 #pragma unroll
-          for (int e = 0; e < 16; e++) {
-            float2 x = make_float2(__uint_as_float(s[32 * c + 2 * e]),
-                                   __uint_as_float(s[32 * c + 2 * e + 1]));
-            x = ffma2(x, sc2, nb2);
-            x.x = pa_exp2(x.x);
-            x.y = pa_exp2(x.y);
-            sum = fadd2(sum, x);
-            p[e] = pack_bf16(x.x, x.y);
-          }
-          pw_st16(tS + 16 * c, p);
-        }
+        for (int e = 32; e < 48; e++) weigh(e);
+        pw_st16(tS + 32, s + 32);
+#pragma unroll
+        for (int e = 48; e < 52; e++) weigh(e);
+        hand_on(0);
+#pragma unroll
+        for (int e = 52; e < 64; e++) weigh(e);
+        pw_st16(tS + 48, s + 48);
+        const float2 sum = fadd2(sums[0], sums[1]);
+        hand_on(1);
         l += sum.x + sum.y;
-        pw_wait_st();
-        tc_fence_before();
-        tc_mbar_arrive(p_full + t);
       }
       if (!ok) break;
-      if (I.nk > 0 && !pw_wait(o_full + t, (n_t + I.nk - 1) & 1)) {
-        ok = false;
-        break;
+      if (I.nk > 0) {
+        if (!pw_wait(o_full + t, n_item & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        give_back(v_empty + (n_tile + I.nk - 1) % ST);
+        if (row == 0) tc_mbar_arrive(q_empty);
+        n_item++;
       }
-      tc_fence_after();
       n_tile += I.nk;
       n_t += I.nk;
       const bool on = r < I.R;
