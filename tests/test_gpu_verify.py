@@ -119,6 +119,20 @@ def test_equal_distributions_accept_everything():
     assert (counts == 5).all() and np.array_equal(out[:, :4], x.numpy())
 
 
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_close_tests_are_decided_exactly(with_draft):
+    """Uniforms within 1e-6 of p / q on either side: closer than sums in 32 bits decide. With one
+    drafted token after another of that kind, accepted and refused."""
+    n, k, V = 24, 4, 20000
+    t, d, x, u = _inputs(n, k, V, seed=9)
+    p = torch.softmax(t[:, :k].double(), -1).gather(2, x[..., None])[..., 0]
+    q = torch.softmax(d.double(), -1).gather(2, x[..., None])[..., 0] if with_draft else 1.0
+    side = torch.tensor([[1 - 1e-6 if (b >> i) & 1 else 1 + 1e-6 for i in range(k)]
+                         for b in range(n)], dtype=torch.float64)
+    u[:, :k] = (p / q * side).float().clamp(max=0.9999)
+    _compare(t, d if with_draft else None, x, 1.0, u)
+
+
 def test_emitted_tokens_follow_the_target():
     """The first emitted token of many sequences with one distribution: its counts against n p.
     Each count is binomial; six of its standard deviations, and one, bound all 12 with a chance of

@@ -4,20 +4,29 @@
 // A token is decided by comparisons of sums over the vocabulary, and the draw
 // by where a running sum passes a point; a sum in 32 bits is off by about
 // 1e-7 of the total, and with tens of thousands of steps per row that picks a
-// neighbouring token every few dozen draws. So weights and sums hold 64 bits.
-// The weight 2^y of a logit takes eleven fp64 operations: y = n / 64 + f / 64
+// neighbouring token every few dozen draws. So what decides holds 64 bits, and
+// 32 bits only where a bound on their error shows that they decide alike:
+//
+// k_verify_rows reads every logit row once: a block takes VF_CHUNK logits of a
+// row, finds their maximum and the sum of their weights relative to it, in 32
+// bits. With the argument of 2^y rounded twice (2^-23 |y|), the special-function
+// unit (2^-22) and sums of 16 + 8 terms, a row's sum is off by less than
+// 2^-22 + 2^-23 * (mean of |y| under the weights, at most log2 of the
+// vocabulary <= 24 bits) + 24 * 2^-24 < 2^-17.6 of itself.
+//
+// k_verify_draw, a cluster of eight blocks per sequence: every block joins the
+// rows' partial sums and makes the tests u q(x) Zp < p(x) Zq with 64-bit
+// weights of the drafted words; one whose sides are closer than VF_CLOSE (twice
+// both sums' bounds) is decided by exact sums. Of the row to draw from each
+// block weighs its eighth in 64 bits (the exact sums first, if drawn from the
+// difference), stores its sum into every block's shared memory, and the one in
+// whose part the point falls walks to it. No block reads another's memory, so
+// none has to stay for its peers after the last barrier.
+//
+// The 64-bit weight 2^y takes eleven fp64 operations: y = n / 64 + f / 64
 // with |f| <= 1/2 (rounded by adding 1.5 * 2^52), 2^(n / 64) from a table of
 // 64 entries and the exponent field, 2^(f / 64) from the exponential series to
 // the fourth power, whose next term is below (ln 2 / 128)^5 / 120 = 4e-14.
-//
-// k_verify_rows reads every logit row once: a block takes VF_CHUNK logits of a
-// row, finds their maximum and the sum of their weights relative to it. Bound
-// by memory (the fp64 pipe needs about as long as the reads).
-// k_verify_draw, a cluster of eight blocks per sequence: every block joins the
-// rows' partial sums and makes the tests; then each weighs its eighth of the
-// row to draw from and stores its sum into every block's shared memory, and the
-// one in whose part the point falls walks to it. No block reads another's
-// memory, so none has to stay for its peers after the last barrier.
 #include <cmath>
 
 #include "paged.cuh"
@@ -30,6 +39,8 @@ constexpr int VF_PER = 16;                       // logits of a thread
 constexpr int VF_CHUNK = VF_THREADS * VF_PER;    // logits of a block
 constexpr int VF_MAX_K = 32;
 constexpr int VF_CLUSTER = 8;
+constexpr int VF_AHEAD = 8;                      // logits of a row a lane fetches together
+constexpr double VF_CLOSE = 1.0 / 32768;         // 2^-15 > 4 * 2^-17.6
 
 struct RowPart {
   double sum;  // of weights relative to max
@@ -43,7 +54,8 @@ struct VerifyArgs {
   const int *tokens, *lens;
   const float *uniforms;
   int n, k, V, chunks;
-  double per64;  // 64 * log2(e) / temperature; 0: greedy
+  double per64;  // 64 * log2(e) / temperature
+  float per1;    // log2(e) / temperature
   RowPart *parts;  // [n][2 k + 1][chunks]: target rows 0 .. k, then draft rows
   int *out, *counts;
 };
@@ -97,13 +109,17 @@ __device__ __forceinline__ void take_max(float &m, int &arg, float m2, int a2) {
   }
 }
 
+__device__ __forceinline__ float exp2_sfu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool GREEDY>
 __global__ void __launch_bounds__(VF_THREADS) k_verify_rows(const VerifyArgs A) {
-  __shared__ double table[64];
-  __shared__ float s_m[VF_WARPS];
+  __shared__ float s_m[VF_WARPS], s_s[VF_WARPS];
   __shared__ int s_a[VF_WARPS];
-  __shared__ double s_s[VF_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  fill_table(table);
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.z, row = blockIdx.y, len = draft_len(A, b);
@@ -111,42 +127,71 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify_rows(const VerifyArgs A) 
   const int i = draft ? row - A.k - 1 : row;
   if (draft ? i >= len : i > len) return;
   const float *src = draft ? A.draft + b * A.d_seq + i * A.d_pos : A.target + b * A.t_seq + i * A.t_pos;
-  const int v0 = blockIdx.x * VF_CHUNK + tid;
+  const int v0 = blockIdx.x * VF_CHUNK;
   float x[VF_PER];
+  // place of x[j]: four neighbours a load where the row allows it
+  const bool fours = ((uintptr_t)src & 15) == 0 && v0 + VF_CHUNK <= A.V;
+  auto place = [&](int j) {
+    return v0 + (fours ? ((j >> 2) * VF_THREADS + tid) * 4 + (j & 3) : j * VF_THREADS + tid);
+  };
+  if (fours) {
 #pragma unroll
-  for (int j = 0; j < VF_PER; j++) {
-    const int v = v0 + j * VF_THREADS;
-    x[j] = v < A.V ? logit(src[v]) : -INFINITY;
+    for (int j = 0; j < VF_PER / 4; j++) {
+      const float4 y = *reinterpret_cast<const float4 *>(src + v0 + (j * VF_THREADS + tid) * 4);
+      x[4 * j] = y.x, x[4 * j + 1] = y.y, x[4 * j + 2] = y.z, x[4 * j + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VF_PER; j++) x[j] = place(j) < A.V ? src[place(j)] : -INFINITY;
   }
   float m = -INFINITY;
   int arg = A.V;
 #pragma unroll
-  for (int j = 0; j < VF_PER; j++)
-    if (x[j] > m) {
+  for (int j = 0; j < VF_PER; j++) {
+    x[j] = fmaxf(x[j], -INFINITY);  // NaN: no weight
+    if (!GREEDY)
+      m = fmaxf(m, x[j]);
+    else if (x[j] > m || (x[j] == m && place(j) < arg && m > -INFINITY)) {
       m = x[j];
-      arg = v0 + j * VF_THREADS;
+      arg = place(j);
     }
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    take_max(m, arg, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, arg, o));
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(FULL_MASK, m, o);
+    if (GREEDY)
+      take_max(m, arg, m2, __shfl_xor_sync(FULL_MASK, arg, o));
+    else
+      m = fmaxf(m, m2);
+  }
   if (lane == 0) {
     s_m[warp] = m;
     s_a[warp] = arg;
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < VF_WARPS; w++) take_max(m, arg, s_m[w], s_a[w]);
-  double sum = 0.0;
-  if (A.per64 > 0.0) {
+  for (int w = 0; w < VF_WARPS; w++) {
+    if (GREEDY)
+      take_max(m, arg, s_m[w], s_a[w]);
+    else
+      m = fmaxf(m, s_m[w]);
+  }
+  float sum = 0.f;
+  if (!GREEDY) {
+    if (isinf(m)) {
 #pragma unroll
-    for (int j = 0; j < VF_PER; j++) sum += weight_of(x[j], m, A.per64, table);
-    sum = warp_sum64(sum);
+      for (int j = 0; j < VF_PER; j++) sum += m > 0.f && x[j] == m ? 1.f : 0.f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < VF_PER; j++) sum += exp2_sfu((x[j] - m) * A.per1);
+    }
+    sum = warp_sum(sum);
     if (lane == 0) s_s[warp] = sum;
     __syncthreads();
   }
   if (tid == 0) {
     double total = 0.0;
-    if (A.per64 > 0.0)
+    if (!GREEDY)
       for (int w = 0; w < VF_WARPS; w++) total += s_s[w];
     A.parts[((size_t)b * (2 * A.k + 1) + row) * A.chunks + blockIdx.x] = {total, m, arg};
   }
@@ -171,7 +216,8 @@ __device__ __forceinline__ RowSum join_row(const VerifyArgs &A, int b, int row) 
   double s = 0.0;
   for (int c = lane; c < A.chunks; c += 32) {
     const float mc = p[c].max;
-    s += p[c].sum * (mc == m ? 1.0 : exp2(((double)mc - (double)m) * A.per64 / 64.0));
+    if (A.per64 > 0.0)
+      s += p[c].sum * (mc == m ? 1.0 : exp2(((double)mc - (double)m) * A.per64 / 64.0));
   }
   return {m == -INFINITY ? 0.0 : warp_sum64(s), m, arg};
 }
@@ -191,13 +237,17 @@ __device__ __forceinline__ void store_in_block(double *place, int rank, double v
   asm volatile("st.shared::cluster.f64 [%0], %1;\n" ::"r"(addr), "d"(v) : "memory");
 }
 
-template <bool DRAFT>  // whether the draft's distribution takes part
+enum { VF_DRAWN = 0, VF_DRAFTED = 1, VF_GREEDY = 2 };
+
+// MODE: greedy, or whether the draft's distribution takes part.
+template <int MODE>
 __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     k_verify_draw(const VerifyArgs A) {
+  constexpr bool DRAFT = MODE == VF_DRAFTED;
   __shared__ double table[64];
   __shared__ RowSum s_t[VF_MAX_K + 1], s_d[VF_MAX_K];
   __shared__ int s_first, s_len;
-  __shared__ double s_w[VF_WARPS], s_all[2][VF_CLUSTER];
+  __shared__ double s_w[2][VF_WARPS], s_all[2][2][VF_CLUSTER];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / VF_CLUSTER, rank = blockIdx.x % VF_CLUSTER;
   fill_table(table);
@@ -214,8 +264,6 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
   }
   __syncthreads();
   len = s_len;
-  if (tid == 0) s_first = len;
-  const bool greedy = !(A.per64 > 0.0);
   for (int i = warp; i <= len; i += VF_WARPS) {
     const RowSum s = join_row(A, b, i);
     if (lane == 0) s_t[i] = s;
@@ -226,35 +274,129 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
       if (lane == 0) s_d[i] = s;
     }
   __syncthreads();
-  if (tid < len) {
-    const int x = A.tokens[b * A.k + tid];
-    const RowSum T = s_t[tid];
-    bool fine;
-    if (greedy) {
-      fine = x == T.arg;
-    } else {
-      const double wp = weight_of(logit(A.target[b * A.t_seq + tid * A.t_pos + x]), T.max,
-                                  A.per64, table);
-      double wq = 1.0, zq = 1.0;
-      if (DRAFT) {
-        const RowSum D = s_d[tid];
-        wq = weight_of(logit(A.draft[b * A.d_seq + tid * A.d_pos + x]), D.max,
-                       A.per64, table);
-        zq = D.sum > 0.0 ? D.sum : 1.0;
+
+  // The two sides of test i, u q(x) Zp < p(x) Zq, without Zp and Zq: every lane
+  // of every block computes the same.
+  auto sides = [&](int i, double &l, double &r) {
+    const int x = A.tokens[b * A.k + i];
+    r = weight_of(logit(A.target[b * A.t_seq + i * A.t_pos + x]), s_t[i].max, A.per64, table);
+    l = (double)A.uniforms[(size_t)b * (A.k + 1) + i];
+    if (DRAFT)
+      l *= weight_of(logit(A.draft[b * A.d_seq + i * A.d_pos + x]), s_d[i].max, A.per64, table);
+  };
+  // Lowest index from `from` on that is not surely accepted (len: none); `close`
+  // where the 32-bit sums do not decide it.
+  bool close = false;
+  auto first_open = [&](int from) {
+    if (tid == 0) s_first = 2 * len;
+    __syncthreads();
+    if (tid >= from && tid < len) {
+      if (MODE == VF_GREEDY) {
+        if (A.tokens[b * A.k + tid] != s_t[tid].arg) atomicMin(&s_first, 2 * tid);
+      } else {
+        double l, r;
+        sides(tid, l, r);
+        l *= s_t[tid].sum;
+        if (DRAFT) r *= s_d[tid].sum > 0.0 ? s_d[tid].sum : 1.0;
+        const bool near = fabs(l - r) <= VF_CLOSE * fmax(l, r) && fmax(l, r) > 0.0;
+        if (near)
+          atomicMin(&s_first, 2 * tid + 1);
+        else if (!(l < r))
+          atomicMin(&s_first, 2 * tid);
       }
-      fine = (double)A.uniforms[(size_t)b * (A.k + 1) + tid] * wq * T.sum < wp * zq;
     }
-    if (!fine) atomicMin(&s_first, tid);
+    __syncthreads();
+    const int f = s_first;
+    __syncthreads();
+    close = f & 1;
+    return f >> 1;
+  };
+
+  // this block's part of a row: warps side by side, 32 logits a step
+  const int steps = (A.V + 31) / 32;
+  const int per_warp = (steps + VF_CLUSTER * VF_WARPS - 1) / (VF_CLUSTER * VF_WARPS);
+  const int first = (rank * VF_WARPS + warp) * per_warp, last = min(steps, first + per_warp);
+  int exchange = 0;
+  double all_a[VF_CLUSTER], all_b[VF_CLUSTER];
+  // The blocks' sums of a (and b), from each warp's, to every block.
+  auto share = [&](double va, double vb) {
+    va = warp_sum64(va);
+    vb = warp_sum64(vb);
+    if (lane == 0) {
+      s_w[0][warp] = va;
+      s_w[1][warp] = vb;
+    }
+    __syncthreads();
+    const int e = exchange++ & 1;
+    if (tid < 2 * VF_CLUSTER) {
+      const int which = tid / VF_CLUSTER;
+      double sum = 0.0;
+      for (int w = 0; w < VF_WARPS; w++) sum += s_w[which][w];
+      store_in_block(&s_all[e][which][rank], tid % VF_CLUSTER, sum);
+    }
+    __syncthreads();
+    cluster_barrier();
+#pragma unroll
+    for (int c = 0; c < VF_CLUSTER; c++) {
+      all_a[c] = s_all[e][0][c];
+      all_b[c] = s_all[e][1][c];
+    }
+  };
+  auto total_of = [](const double v[VF_CLUSTER]) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < VF_CLUSTER; c++) s += v[c];
+    return s;
+  };
+
+  // tests; every block of the cluster takes the same turns
+  int j = first_open(0);
+  double zp = 0.0, zq = 0.0;
+  if (MODE != VF_GREEDY) {
+    while (j < len) {
+      // exact sums of row j: they decide a close test, and a draw from the
+      // difference needs them
+      const RowSum T = s_t[j], D = DRAFT ? s_d[j] : RowSum{0.0, -INFINITY, 0};
+      const float *tr = A.target + b * A.t_seq + j * A.t_pos;
+      const float *dr = DRAFT ? A.draft + b * A.d_seq + j * A.d_pos : nullptr;
+      double a = 0.0, d = 0.0;
+      for (int s0 = first; s0 < last; s0 += VF_AHEAD) {
+        float x[VF_AHEAD], y[VF_AHEAD];
+#pragma unroll
+        for (int e = 0; e < VF_AHEAD; e++) {
+          const int v = (s0 + e) * 32 + lane;
+          const bool on = s0 + e < last && v < A.V;
+          x[e] = on ? logit(tr[v]) : -INFINITY;
+          if (DRAFT) y[e] = on ? logit(dr[v]) : -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < VF_AHEAD; e++) {
+          a += weight_of(x[e], T.max, A.per64, table);
+          if (DRAFT) d += weight_of(y[e], D.max, A.per64, table);
+        }
+      }
+      share(a, d);
+      zp = total_of(all_a);
+      zq = total_of(all_b);
+      if (close) {
+        double l, r;
+        sides(j, l, r);
+        if (l * zp < r * (DRAFT && zq > 0.0 ? zq : 1.0)) {
+          j = first_open(j + 1);
+          continue;
+        }
+      }
+      break;
+    }
   }
-  __syncthreads();
-  const int j = s_first;
+
   const RowSum T = s_t[j];
   int *out = A.out + (size_t)b * (A.k + 1);
   if (rank == 0 && tid <= A.k) {
     if (tid < j) out[tid] = A.tokens[b * A.k + tid];
     if (tid > j) out[tid] = -1;
   }
-  if (greedy || T.max == -INFINITY) {  // the whole cluster: nothing to draw
+  if (MODE == VF_GREEDY || T.max == -INFINITY) {  // the whole cluster: nothing to draw
     if (rank == 0 && tid == 0) {
       const bool none = T.max == -INFINITY;
       out[j] = none ? -1 : T.arg;
@@ -263,89 +405,90 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     return;
   }
 
-  // weights of this block's part of the row: warps side by side, 32 logits a step
-  const bool refused = j < len;
-  const float *tr = A.target + b * A.t_seq + j * A.t_pos;
   // A draft row is addressed whether or not it takes part: nvcc 12.9 compiled
   // `condition ? row : nullptr` here to an address that ignored the condition.
   const int dj = min(j, max(len - 1, 0));
+  const float *tr = A.target + b * A.t_seq + j * A.t_pos;
   const float *dr = DRAFT ? A.draft + b * A.d_seq + dj * A.d_pos : nullptr;
   const int skip = !DRAFT && A.k > 0 ? A.tokens[b * A.k + min(j, A.k - 1)] : -1;
-  const RowSum D = DRAFT ? s_d[dj] : RowSum{0.0, -INFINITY, 0};
-  const double over = D.sum > 0.0 ? T.sum / D.sum : 0.0;  // the draft's weights on the target's scale
-  const int steps = (A.V + 31) / 32;
-  const int per_warp = (steps + VF_CLUSTER * VF_WARPS - 1) / (VF_CLUSTER * VF_WARPS);
-  const int first = (rank * VF_WARPS + warp) * per_warp, last = min(steps, first + per_warp);
+  const float dmax = DRAFT ? s_d[dj].max : 0.f;
+  const double over = DRAFT && zq > 0.0 ? zp / zq : 0.0;  // the draft's weights on the target's scale
   const double point01 = (double)A.uniforms[(size_t)b * (A.k + 1) + A.k];
-  bool residual = refused;
+  bool residual = j < len;
   for (int pass = 0; pass < 2; pass++) {
-    auto weight = [&](int v) {
-      if (v >= A.V || (!DRAFT && residual && v == skip)) return 0.0;
-      double w = weight_of(logit(tr[v]), T.max, A.per64, table);
-      if (DRAFT && residual)
-        w = fmax(w - weight_of(logit(dr[v]), D.max, A.per64, table) * over, 0.0);
-      return w;
+    // weights of VF_AHEAD steps from s0 on
+    auto weights = [&](int s0, double w[VF_AHEAD]) {
+      float x[VF_AHEAD], y[VF_AHEAD];
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) {
+        const int v = (s0 + e) * 32 + lane;
+        const bool on = s0 + e < last && v < A.V && !(!DRAFT && residual && v == skip);
+        x[e] = on ? logit(tr[v]) : -INFINITY;
+        if (DRAFT) y[e] = on && residual ? logit(dr[v]) : -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) {
+        w[e] = weight_of(x[e], T.max, A.per64, table);
+        if (DRAFT && residual)
+          w[e] = fmax(w[e] - weight_of(y[e], dmax, A.per64, table) * over, 0.0);
+      }
     };
     double mine = 0.0;
-#pragma unroll 4
-    for (int s = first; s < last; s++) mine += weight(s * 32 + lane);
-    mine = warp_sum64(mine);
-    if (lane == 0) s_w[warp] = mine;
-    __syncthreads();
-    if (tid < VF_CLUSTER) {
-      double sum = 0.0;
-      for (int w = 0; w < VF_WARPS; w++) sum += s_w[w];
-      store_in_block(&s_all[pass][rank], tid, sum);
-    }
-    __syncthreads();
-    cluster_barrier();
-    // the first block whose running sum passes the point; rounding aside there is one
-    double total = 0.0, before = 0.0, base = 0.0;
-    int owner = -1, heavy = -1;
-    double all[VF_CLUSTER];
+    for (int s0 = first; s0 < last; s0 += VF_AHEAD) {
+      double w[VF_AHEAD];
+      weights(s0, w);
 #pragma unroll
-    for (int c = 0; c < VF_CLUSTER; c++) {
-      all[c] = s_all[pass][c];
-      total += all[c];
-      if (all[c] > 0.0) heavy = c;
+      for (int e = 0; e < VF_AHEAD; e++) mine += w[e];
     }
+    share(mine, 0.0);
+    // the first block whose running sum passes the point; rounding aside there is one
+    const double total = total_of(all_a);
+    double before = 0.0, base = 0.0;
+    int owner = -1, heavy = -1;
+#pragma unroll
+    for (int c = 0; c < VF_CLUSTER; c++)
+      if (all_a[c] > 0.0) heavy = c;
     const double point = point01 * total;
 #pragma unroll
     for (int c = 0; c < VF_CLUSTER; c++) {
-      if (owner < 0 && (base + all[c] > point || c == heavy)) {
+      if (owner < 0 && (base + all_a[c] > point || c == heavy)) {
         owner = c;
         before = base;
       }
-      base += all[c];
+      base += all_a[c];
     }
     if (total > 0.0) {
       if (rank != owner) return;
       int ow = -1, hw = -1;
       double wb = before, at = before;
       for (int w = 0; w < VF_WARPS; w++)
-        if (s_w[w] > 0.0) hw = w;
+        if (s_w[0][w] > 0.0) hw = w;
       for (int w = 0; w < VF_WARPS; w++) {
-        if (ow < 0 && (wb + s_w[w] > point || w == hw)) {
+        if (ow < 0 && (wb + s_w[0][w] > point || w == hw)) {
           ow = w;
           at = wb;
         }
-        wb += s_w[w];
+        wb += s_w[0][w];
       }
       if (warp != ow) return;
       int token = -1, weighted = -1;
-      for (int s = first; s < last && token < 0; s++) {
-        const double w = weight(s * 32 + lane);
-        double run = w;
+      for (int s0 = first; s0 < last && token < 0; s0 += VF_AHEAD) {
+        double w[VF_AHEAD];
+        weights(s0, w);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(FULL_MASK, run, o);
-          if (lane >= o) run += y;
+        for (int e = 0; e < VF_AHEAD; e++) {
+          double run = w[e];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(FULL_MASK, run, o);
+            if (lane >= o) run += y;
+          }
+          const unsigned passed = __ballot_sync(FULL_MASK, w[e] > 0.0 && at + run > point);
+          const unsigned some = __ballot_sync(FULL_MASK, w[e] > 0.0);
+          if (passed && token < 0) token = (s0 + e) * 32 + __ffs(passed) - 1;
+          if (some) weighted = (s0 + e) * 32 + 31 - __clz(some);
+          at += __shfl_sync(FULL_MASK, run, 31);
         }
-        const unsigned passed = __ballot_sync(FULL_MASK, w > 0.0 && at + run > point);
-        const unsigned some = __ballot_sync(FULL_MASK, w > 0.0);
-        if (passed) token = s * 32 + __ffs(passed) - 1;
-        if (some) weighted = s * 32 + 31 - __clz(some);
-        at += __shfl_sync(FULL_MASK, run, 31);
       }
       if (lane == 0) {
         out[j] = token >= 0 ? token : weighted;
@@ -405,6 +548,7 @@ RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_p
   A.V = vocab;
   A.chunks = verify_chunks(vocab);
   A.per64 = per64;
+  A.per1 = (float)(per64 / 64.0);
   A.parts = static_cast<RowPart *>(workspace);
   A.out = tokens;
   A.counts = counts;
@@ -419,11 +563,13 @@ RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_p
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = st == nullptr ? 0 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_verify_rows, A);
+  cudaError_t e = greedy ? cudaLaunchKernelEx(&cfg, k_verify_rows<true>, A)
+                         : cudaLaunchKernelEx(&cfg, k_verify_rows<false>, A);
   if (e == cudaSuccess) {
     cfg.gridDim = dim3(n * VF_CLUSTER);
-    e = drafted ? cudaLaunchKernelEx(&cfg, k_verify_draw<true>, A)
-                : cudaLaunchKernelEx(&cfg, k_verify_draw<false>, A);
+    e = greedy    ? cudaLaunchKernelEx(&cfg, k_verify_draw<VF_GREEDY>, A)
+        : drafted ? cudaLaunchKernelEx(&cfg, k_verify_draw<VF_DRAFTED>, A)
+                  : cudaLaunchKernelEx(&cfg, k_verify_draw<VF_DRAWN>, A);
   }
   return cuda_status_internal(e, __LINE__);
 }
