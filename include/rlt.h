@@ -627,7 +627,8 @@ RLT_API size_t rlt_verify_workspace_bytes(int n, int k, int vocab);
  *   whose cumulative weight exceeds uniforms[b][k] * (sum of weights).
  * temperature 0: x_i is accepted if it is the target's first maximum, and the
  * new token is that maximum (draft and uniforms unused). Tests and sums hold 64
- * bits. NaN logits count as -inf (weight 0); where +inf occurs, those entries
+ * bits; a weight below 2^-1000 of its row's largest is none. NaN logits count as
+ * -inf (no weight); where +inf occurs, those entries
  * share the weight. A row without any weight has no token: it ends the
  * sequence's answer there.
  *   target   device float32, element (b, i, v) at b * target_seq + i * target_pos + v,

@@ -2,6 +2,7 @@
 the 8-bit elements, a cache in pages, chunk attention, draft verification. They share nothing with
 the library but the layouts."""
 import math
+from decimal import Decimal, getcontext
 
 import numpy as np
 import torch
@@ -143,9 +144,10 @@ def attend_bound(ref, mass, size, dh, dtype):
     return b + 1e-30
 
 
-def verify64(target, draft, tokens, lens, u, tau):
+def verify64(target, draft, tokens, lens, u, tau, digits=0):
     """float64 numpy arrays; tokens [n][k]. Returns (tokens, counts, margin): margin the least
-    relative distance of a comparison from its border."""
+    relative distance of a comparison from its border. digits: of decimal arithmetic instead of
+    float64, where 1 - 1e-38 and 1 have to differ."""
     n, k1, V = target.shape
     k = k1 - 1
     out, counts, margin = np.full((n, k1), -1, np.int64), np.zeros(n, np.int64), math.inf
@@ -157,9 +159,18 @@ def verify64(target, draft, tokens, lens, u, tau):
             return np.zeros(V)
         if top == np.inf:
             w = (x == np.inf).astype(np.float64)
+        elif digits:
+            t = Decimal(float(tau))
+            w = np.array([Decimal(0) if v == -np.inf else ((Decimal(float(v)) - Decimal(float(top)))
+                                                           / t).exp() for v in x])
         else:
             w = np.exp((x - top) / tau)
+        w[w < 2.0 ** -1000] *= 0
         return w / w.sum()
+
+    if digits:
+        getcontext().prec = digits
+        u = np.array([[Decimal(float(v)) for v in row] for row in u])
 
     for b in range(n):
         L = min(max(int(lens[b]), 0), k)
@@ -187,11 +198,11 @@ def verify64(target, draft, tokens, lens, u, tau):
                 if draft is not None:
                     q = weights(draft[b, j])
                 else:
-                    q = np.zeros(V)
-                    q[x] = 1.0
+                    q = np.zeros(V) * p[0]
+                    q[x] += 1
                 a, c = u[b, j] * q[x], p[x]
                 if max(a, c) > 0:
-                    margin = min(margin, abs(a - c) / max(a, c) if a != c else margin)
+                    margin = min(margin, float(abs(a - c) / max(a, c)) if a != c else margin)
                 if a < c:
                     out[b, j] = x
                     j += 1
@@ -204,7 +215,7 @@ def verify64(target, draft, tokens, lens, u, tau):
                 break
             cum = np.cumsum(p)
             t = u[b, k] * cum[-1]
-            margin = min(margin, np.abs(cum - t).min() / cum[-1])
+            margin = min(margin, float(np.abs(cum - t).min() / cum[-1]))
             v = int(np.searchsorted(cum, t, side="right"))
             out[b, j] = min(v, int(np.flatnonzero(p).max()))
             counts[b] = j + 1

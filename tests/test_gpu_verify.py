@@ -22,13 +22,14 @@ def _run(target, draft, tokens, tau, u, lens=None, position_major=False):
     return out.cpu().numpy(), counts.cpu().numpy()
 
 
-def _compare(target, draft, tokens, tau, u, lens=None, **kw):
+def _compare(target, draft, tokens, tau, u, lens=None, digits=0, **kw):
     n, k = target.shape[0], target.shape[1] - 1
     got = _run(target, draft, tokens, tau, u, lens, **kw)
     ref = verify64(target.double().numpy(), None if draft is None else draft.double().numpy(),
                    tokens.numpy() if k else np.zeros((n, 0), np.int64),
                    lens if lens is not None else [k] * n,
-                   np.zeros((n, k + 1)) if u is None else u.double().numpy(), tau)
+                   np.zeros((n, k + 1)) if u is None else u.double().numpy(), tau,
+                   digits)
     # weights of 64 bits, sums of at most 2^17 of them: 2^-52 * 2^17 at the very worst
     assert ref[2] > 2.0 ** -35, "a comparison of this case is too near its border to be decided"
     assert np.array_equal(got[1], ref[1]), (got[1], ref[1])
@@ -111,6 +112,30 @@ def test_huge_logits():
     t = t * 1e30
     x[:, 0] = t[:, 0].argmax(-1)
     _compare(t, t[:, :2].contiguous(), x, 0.5, u)
+
+
+def test_nearly_equal_distributions():
+    """p and q equal to 1e-6, with drafted words of no weight under p: refusals whose difference is
+    tiny everywhere; and many words of equal weights in both."""
+    t, _, x, u = _inputs(6, 2, 3000, seed=10)
+    g = torch.Generator().manual_seed(3)
+    d = t[:, :2] + 1e-6 * torch.randn(t[:, :2].shape, generator=g)
+    for b in range(6):
+        t[b, 0, x[b, 0]] = -math.inf
+    _compare(t, d, x, 1.0, u)
+    t, d, x, u = _inputs(6, 2, 3000, seed=11)
+    t[:, :, ::2] = 1.0
+    d[:, :, ::2] = 1.0
+    _compare(t, d, x, 1.0, u)
+
+
+@pytest.mark.parametrize("tau", [1e-3, 1e-40, 50.0])
+def test_extreme_temperatures(tau):
+    """At 1e-3 a row's p and q are both 1 - 1e-38 or so at one word: its difference, 1.7e-38 in one of
+    these rows, is the draw's whole weight but not in 64 bits, so the reference takes decimals."""
+    t, d, x, u = _inputs(5, 3, 900, seed=12)
+    _compare(t, d, x, float(torch.tensor(tau, dtype=torch.float32)), u,
+             digits=60 if tau == 1e-3 else 0)
 
 
 def test_equal_distributions_accept_everything():

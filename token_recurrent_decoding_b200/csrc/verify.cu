@@ -18,15 +18,23 @@
 // rows' partial sums and makes the tests u q(x) Zp < p(x) Zq with 64-bit
 // weights of the drafted words; one whose sides are closer than VF_CLOSE (twice
 // both sums' bounds) is decided by exact sums. Of the row to draw from each
-// block weighs its eighth in 64 bits (the exact sums first, if drawn from the
-// difference), stores its sum into every block's shared memory, and the one in
-// whose part the point falls walks to it. No block reads another's memory, so
-// none has to stay for its peers after the last barrier.
+// block weighs its eighth in 64 bits, stores its sum into every block's shared
+// memory, and the one in whose part the point falls walks to it. No block reads
+// another's memory, so none has to stay for its peers after the last barrier.
 //
-// The 64-bit weight 2^y takes eleven fp64 operations: y = n / 64 + f / 64
-// with |f| <= 1/2 (rounded by adding 1.5 * 2^52), 2^(n / 64) from a table of
-// 64 entries and the exponent field, 2^(f / 64) from the exponential series to
-// the fourth power, whose next term is below (ln 2 / 128)^5 / 120 = 4e-14.
+// A draw from max(p - q, 0) needs Zp / Zq before a word's weight, and would read
+// and weigh both rows twice. Instead one pass adds up, next to both sums, the
+// p and q weights of the words whose difference is surely positive under the
+// 32-bit sums, and keeps the few words too close to tell (VF_NEAR) aside: with
+// the exact ratio r the part's weight is (sum of p) - r (sum of q) + what the
+// words aside give. Where more are close than there is room for (p and q nearly
+// equal) the rows are weighed again.
+//
+// The 64-bit weight 2^y takes ten fp64 operations: y = n / 256 + f / 256 with
+// |f| <= 1/2 (rounded by adding 1.5 * 2^52), 2^(n / 256) from a table of 256
+// entries and the exponent field, 2^(f / 256) from the exponential series to
+// the third power, whose next term is below (ln 2 / 512)^4 / 24 = 1.4e-13.
+// Weights below 2^-1000 are nothing.
 #include <cmath>
 
 #include "paged.cuh"
@@ -41,6 +49,8 @@ constexpr int VF_MAX_K = 32;
 constexpr int VF_CLUSTER = 8;
 constexpr int VF_AHEAD = 8;                      // logits of a row a lane fetches together
 constexpr double VF_CLOSE = 1.0 / 32768;         // 2^-15 > 4 * 2^-17.6
+constexpr double VF_NEAR = 1.0 / 16384;          // of p's weight
+constexpr int VF_ASIDE = 16;                     // words of a warp kept aside
 
 struct RowPart {
   double sum;  // of weights relative to max
@@ -54,8 +64,8 @@ struct VerifyArgs {
   const int *tokens, *lens;
   const float *uniforms;
   int n, k, V, chunks;
-  double per64;  // 64 * log2(e) / temperature
-  float per1;    // log2(e) / temperature
+  double per;    // log2(e) / temperature; 0: greedy
+  float per32;   // the same
   RowPart *parts;  // [n][2 k + 1][chunks]: target rows 0 .. k, then draft rows
   int *out, *counts;
 };
@@ -67,32 +77,46 @@ __device__ __forceinline__ int draft_len(const VerifyArgs &A, int b) {
 // NaN has no weight.
 __device__ __forceinline__ float logit(float x) { return x == x ? x : -INFINITY; }
 
-__device__ __forceinline__ void fill_table(double *table) {
-  if (threadIdx.x < 64) table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+__device__ __forceinline__ void fill_table(double table[256]) {
+  table[threadIdx.x] = exp2(threadIdx.x / 256.0);  // blocks of 256 threads
 }
 
-// 2^(t / 64) for t <= 0.
-__device__ __forceinline__ double weight64(double t, const double *table) {
+// Weight of a logit relative to the row's maximum m, whatever they are.
+__device__ __noinline__ double weight_of(float x, float m, double per) {
+  if (isinf(m)) return m > 0.f && x == m ? 1.0 : 0.0;
+  const double y = ((double)x - (double)m) * per;
+  return y > -1000.0 ? exp2(y) : 0.0;
+}
+
+// The same for many logits of one row: the product of a logit is rounded once,
+// with the maximum's product, which all share, so rows whose products are too
+// large for that (and rows of infinities) take weight_of.
+struct RowWeights {
+  float m, lo;   // what lies at or below lo weighs nothing
+  double c, per256;
+  bool plain;
+};
+__device__ __forceinline__ RowWeights row_weights(float m, double per) {
+  const double per256 = 256.0 * per, c = (double)m * per256;
+  return {m, (float)((double)m - 1000.0 / per), c, per256, !isinf(m) && fabs(c) < 1073741824.0};
+}
+// Of plain rows; clamped to lo's (about 2^-1000) from below, NaN too.
+__device__ __forceinline__ double weight_fast(float x, const RowWeights &R, const double *table) {
+  const double t = fma((double)fmaxf(x, R.lo), R.per256, -R.c);
   const double shift = 6755399441055744.0;  // 1.5 * 2^52
   const double r = t + shift;
   const int n = __double2loint(r);
   const double f = t - (r - shift);
-  const double a = 0.010830424696249145;  // ln 2 / 64
-  double p = a * a * a * a / 24;
-  p = fma(p, f, a * a * a / 6);
-  p = fma(p, f, a * a / 2);
+  const double a = 0.0027076061740622863;  // ln 2 / 256
+  double p = fma(a * a * a / 6, f, a * a / 2);
   p = fma(p, f, a);
   p = fma(p, f, 1.0);
-  p *= table[n & 63];
-  p = __hiloint2double(__double2hiint(p) + ((n >> 6) << 20), __double2loint(p));
-  return t > -65000.0 ? p : 0.0;  // 2^-1015: everything smaller counts as nothing
+  p *= table[n & 255];
+  return __hiloint2double(__double2hiint(p) + ((n >> 8) << 20), __double2loint(p));
 }
-
-// Weight of x relative to the row's maximum m. The difference comes first: a
-// product of a large logit would be rounded by more than one.
-__device__ __forceinline__ double weight_of(float x, float m, double per64, const double *table) {
-  if (isinf(m)) return m > 0.f && x == m ? 1.0 : 0.0;
-  return weight64(((double)x - (double)m) * per64, table);
+// Whether a logit weighs anything in its row.
+__device__ __forceinline__ bool weighs(float x, const RowWeights &R) {
+  return R.plain ? x > R.lo : x == x && x > -INFINITY && (!isinf(R.m) || x == R.m);
 }
 
 __device__ __forceinline__ double warp_sum64(double v) {
@@ -183,7 +207,7 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify_rows(const VerifyArgs A) 
       for (int j = 0; j < VF_PER; j++) sum += m > 0.f && x[j] == m ? 1.f : 0.f;
     } else {
 #pragma unroll
-      for (int j = 0; j < VF_PER; j++) sum += exp2_sfu((x[j] - m) * A.per1);
+      for (int j = 0; j < VF_PER; j++) sum += exp2_sfu((x[j] - m) * A.per32);
     }
     sum = warp_sum(sum);
     if (lane == 0) s_s[warp] = sum;
@@ -216,8 +240,8 @@ __device__ __forceinline__ RowSum join_row(const VerifyArgs &A, int b, int row) 
   double s = 0.0;
   for (int c = lane; c < A.chunks; c += 32) {
     const float mc = p[c].max;
-    if (A.per64 > 0.0)
-      s += p[c].sum * (mc == m ? 1.0 : exp2(((double)mc - (double)m) * A.per64 / 64.0));
+    if (A.per > 0.0)
+      s += p[c].sum * (mc == m ? 1.0 : exp2(((double)mc - (double)m) * A.per));
   }
   return {m == -INFINITY ? 0.0 : warp_sum64(s), m, arg};
 }
@@ -241,29 +265,38 @@ enum { VF_DRAWN = 0, VF_DRAFTED = 1, VF_GREEDY = 2 };
 
 // MODE: greedy, or whether the draft's distribution takes part.
 template <int MODE>
-__global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
+__global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS, 3)
     k_verify_draw(const VerifyArgs A) {
   constexpr bool DRAFT = MODE == VF_DRAFTED;
-  __shared__ double table[64];
+  __shared__ double table[256];
   __shared__ RowSum s_t[VF_MAX_K + 1], s_d[VF_MAX_K];
   __shared__ int s_first, s_len;
-  __shared__ double s_w[2][VF_WARPS], s_all[2][2][VF_CLUSTER];
+  __shared__ double s_w[3][VF_WARPS], s_all[2][3][VF_CLUSTER];
+  __shared__ float s_u[VF_MAX_K], s_lt[VF_MAX_K], s_ld[VF_MAX_K];  // of the drafted words
+  __shared__ double2 s_aside[VF_WARPS][VF_ASIDE];  // p and q weights
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / VF_CLUSTER, rank = blockIdx.x % VF_CLUSTER;
-  fill_table(table);
-  __syncthreads();
-  cluster_barrier();  // every block has begun: its shared memory may be written
-  pdl_wait();
+  // The caller's inputs are complete: k_verify_rows waited for them before it
+  // let this kernel begin. Only its sums are waited for below.
   int len = draft_len(A, b);
   if (tid == 0) s_len = len;
   __syncthreads();
   // a drafted token that is none of the vocabulary ends the draft
   if (tid < len) {
     const int x = A.tokens[b * A.k + tid];
-    if (x < 0 || x >= A.V) atomicMin(&s_len, tid);
+    if (x < 0 || x >= A.V) {
+      atomicMin(&s_len, tid);
+    } else if (MODE != VF_GREEDY) {
+      s_u[tid] = A.uniforms[(size_t)b * (A.k + 1) + tid];
+      s_lt[tid] = logit(A.target[b * A.t_seq + tid * A.t_pos + x]);
+      if (DRAFT) s_ld[tid] = logit(A.draft[b * A.d_seq + tid * A.d_pos + x]);
+    }
   }
+  fill_table(table);
   __syncthreads();
+  cluster_barrier();  // every block has begun: its shared memory may be written
   len = s_len;
+  pdl_wait();
   for (int i = warp; i <= len; i += VF_WARPS) {
     const RowSum s = join_row(A, b, i);
     if (lane == 0) s_t[i] = s;
@@ -278,11 +311,9 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
   // The two sides of test i, u q(x) Zp < p(x) Zq, without Zp and Zq: every lane
   // of every block computes the same.
   auto sides = [&](int i, double &l, double &r) {
-    const int x = A.tokens[b * A.k + i];
-    r = weight_of(logit(A.target[b * A.t_seq + i * A.t_pos + x]), s_t[i].max, A.per64, table);
-    l = (double)A.uniforms[(size_t)b * (A.k + 1) + i];
-    if (DRAFT)
-      l *= weight_of(logit(A.draft[b * A.d_seq + i * A.d_pos + x]), s_d[i].max, A.per64, table);
+    r = weight_of(s_lt[i], s_t[i].max, A.per);
+    l = (double)s_u[i];
+    if (DRAFT) l *= weight_of(s_ld[i], s_d[i].max, A.per);
   };
   // Lowest index from `from` on that is not surely accepted (len: none); `close`
   // where the 32-bit sums do not decide it.
@@ -317,18 +348,17 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
   const int per_warp = (steps + VF_CLUSTER * VF_WARPS - 1) / (VF_CLUSTER * VF_WARPS);
   const int first = (rank * VF_WARPS + warp) * per_warp, last = min(steps, first + per_warp);
   int exchange = 0;
-  double all_a[VF_CLUSTER], all_b[VF_CLUSTER];
-  // The blocks' sums of a (and b), from each warp's, to every block.
-  auto share = [&](double va, double vb) {
-    va = warp_sum64(va);
-    vb = warp_sum64(vb);
+  double all[3][VF_CLUSTER];
+  // The blocks' sums of three values, from each lane's, to every block.
+  auto share = [&](double v0, double v1, double v2) {
+    const double v[3] = {warp_sum64(v0), warp_sum64(v1), warp_sum64(v2)};
     if (lane == 0) {
-      s_w[0][warp] = va;
-      s_w[1][warp] = vb;
+#pragma unroll
+      for (int i = 0; i < 3; i++) s_w[i][warp] = v[i];
     }
     __syncthreads();
     const int e = exchange++ & 1;
-    if (tid < 2 * VF_CLUSTER) {
+    if (tid < 3 * VF_CLUSTER) {
       const int which = tid / VF_CLUSTER;
       double sum = 0.0;
       for (int w = 0; w < VF_WARPS; w++) sum += s_w[which][w];
@@ -337,47 +367,94 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     __syncthreads();
     cluster_barrier();
 #pragma unroll
-    for (int c = 0; c < VF_CLUSTER; c++) {
-      all_a[c] = s_all[e][0][c];
-      all_b[c] = s_all[e][1][c];
-    }
+    for (int i = 0; i < 3; i++)
+#pragma unroll
+      for (int c = 0; c < VF_CLUSTER; c++) all[i][c] = s_all[e][i][c];
   };
-  auto total_of = [](const double v[VF_CLUSTER]) {
+  auto total_of = [&](int i) {
     double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < VF_CLUSTER; c++) s += v[c];
+    for (int c = 0; c < VF_CLUSTER; c++) s += all[i][c];
     return s;
+  };
+  // VF_AHEAD steps of a row from s0 on
+  auto fetch = [&](const float *row, int s0, float x[VF_AHEAD]) {
+    if (s0 + VF_AHEAD <= last && (s0 + VF_AHEAD) * 32 <= A.V) {
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) x[e] = row[(s0 + e) * 32 + lane];
+    } else {
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) {
+        const int v = (s0 + e) * 32 + lane;
+        x[e] = s0 + e < last && v < A.V ? row[v] : -INFINITY;
+      }
+    }
+  };
+
+  auto weights_of = [&](const float x[VF_AHEAD], const RowWeights &R, double w[VF_AHEAD]) {
+    if (R.plain) {
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) w[e] = weight_fast(x[e], R, table);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VF_AHEAD; e++) w[e] = weight_of(logit(x[e]), R.m, A.per);
+    }
   };
 
   // tests; every block of the cluster takes the same turns
   int j = first_open(0);
-  double zp = 0.0, zq = 0.0;
+  double zp = 0.0, zq = 0.0, surely = 0.0;  // surely: this lane's part of p - q, see above
+  bool split = false;                       // whether it holds
   if (MODE != VF_GREEDY) {
-    while (j < len) {
+    while (j < len && (DRAFT || close)) {
       // exact sums of row j: they decide a close test, and a draw from the
       // difference needs them
       const RowSum T = s_t[j], D = DRAFT ? s_d[j] : RowSum{0.0, -INFINITY, 0};
+      const RowWeights P = row_weights(T.max, A.per), Q = row_weights(D.max, A.per);
       const float *tr = A.target + b * A.t_seq + j * A.t_pos;
       const float *dr = DRAFT ? A.draft + b * A.d_seq + j * A.d_pos : nullptr;
-      double a = 0.0, d = 0.0;
+      const double ratio = DRAFT && D.sum > 0.0 ? T.sum / D.sum : 0.0;
+      double a = 0.0, d = 0.0, sure_p = 0.0, sure_q = 0.0;
+      int aside = 0;
       for (int s0 = first; s0 < last; s0 += VF_AHEAD) {
         float x[VF_AHEAD], y[VF_AHEAD];
+        fetch(tr, s0, x);
+        if (DRAFT) fetch(dr, s0, y);
+        // all weights first: fp64 operations take long and overlap
+        double wp[VF_AHEAD], wq[VF_AHEAD];
+        weights_of(x, P, wp);
+        if (DRAFT) weights_of(y, Q, wq);
+        unsigned near = 0;
 #pragma unroll
         for (int e = 0; e < VF_AHEAD; e++) {
-          const int v = (s0 + e) * 32 + lane;
-          const bool on = s0 + e < last && v < A.V;
-          x[e] = on ? logit(tr[v]) : -INFINITY;
-          if (DRAFT) y[e] = on ? logit(dr[v]) : -INFINITY;
+          a += wp[e];
+          if (DRAFT) {
+            d += wq[e];
+            const double gap = fma(-ratio, wq[e], wp[e]);
+            if (weighs(x[e], P)) {
+              if (fabs(gap) <= VF_NEAR * wp[e]) {
+                near |= 1u << e;
+              } else if (gap > 0.0) {
+                sure_p += wp[e];
+                sure_q += wq[e];
+              }
+            }
+          }
         }
+        if (DRAFT && __any_sync(FULL_MASK, near != 0)) {
 #pragma unroll
-        for (int e = 0; e < VF_AHEAD; e++) {
-          a += weight_of(x[e], T.max, A.per64, table);
-          if (DRAFT) d += weight_of(y[e], D.max, A.per64, table);
+          for (int e = 0; e < VF_AHEAD; e++) {
+            const unsigned nears = __ballot_sync(FULL_MASK, near >> e & 1);
+            const int at = aside + __popc(nears & ((1u << lane) - 1));
+            if ((near >> e & 1) && at < VF_ASIDE) s_aside[warp][at] = make_double2(wp[e], wq[e]);
+            aside += __popc(nears);
+          }
         }
       }
-      share(a, d);
-      zp = total_of(all_a);
-      zq = total_of(all_b);
+      share(a, d, lane == 0 && aside > VF_ASIDE ? 1.0 : 0.0);
+      zp = total_of(0);
+      zq = total_of(1);
+      split = DRAFT && total_of(2) == 0.0;
       if (close) {
         double l, r;
         sides(j, l, r);
@@ -385,6 +462,12 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
           j = first_open(j + 1);
           continue;
         }
+      }
+      const double over = zq > 0.0 ? zp / zq : 0.0;
+      surely = sure_p - over * sure_q;
+      if (lane < aside && lane < VF_ASIDE) {
+        const double2 w = s_aside[warp][lane];
+        surely += fmax(w.x - w.y * over, 0.0);
       }
       break;
     }
@@ -411,7 +494,8 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
   const float *tr = A.target + b * A.t_seq + j * A.t_pos;
   const float *dr = DRAFT ? A.draft + b * A.d_seq + dj * A.d_pos : nullptr;
   const int skip = !DRAFT && A.k > 0 ? A.tokens[b * A.k + min(j, A.k - 1)] : -1;
-  const float dmax = DRAFT ? s_d[dj].max : 0.f;
+  const RowWeights P = row_weights(T.max, A.per);
+  const RowWeights Q = row_weights(DRAFT ? s_d[dj].max : -INFINITY, A.per);
   const double over = DRAFT && zq > 0.0 ? zp / zq : 0.0;  // the draft's weights on the target's scale
   const double point01 = (double)A.uniforms[(size_t)b * (A.k + 1) + A.k];
   bool residual = j < len;
@@ -419,45 +503,46 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     // weights of VF_AHEAD steps from s0 on
     auto weights = [&](int s0, double w[VF_AHEAD]) {
       float x[VF_AHEAD], y[VF_AHEAD];
+      fetch(tr, s0, x);
+      if (DRAFT && residual) fetch(dr, s0, y);
+      double q[VF_AHEAD];
+      weights_of(x, P, w);
+      if (DRAFT && residual) weights_of(y, Q, q);
 #pragma unroll
       for (int e = 0; e < VF_AHEAD; e++) {
-        const int v = (s0 + e) * 32 + lane;
-        const bool on = s0 + e < last && v < A.V && !(!DRAFT && residual && v == skip);
-        x[e] = on ? logit(tr[v]) : -INFINITY;
-        if (DRAFT) y[e] = on && residual ? logit(dr[v]) : -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < VF_AHEAD; e++) {
-        w[e] = weight_of(x[e], T.max, A.per64, table);
-        if (DRAFT && residual)
-          w[e] = fmax(w[e] - weight_of(y[e], dmax, A.per64, table) * over, 0.0);
+        if (!weighs(x[e], P) || (!DRAFT && residual && (s0 + e) * 32 + lane == skip)) w[e] = 0.0;
+        if (DRAFT && residual) w[e] = fmax(w[e] - q[e] * over, 0.0);
       }
     };
     double mine = 0.0;
-    for (int s0 = first; s0 < last; s0 += VF_AHEAD) {
-      double w[VF_AHEAD];
-      weights(s0, w);
+    if (residual && split) {
+      mine = surely;
+    } else {
+      for (int s0 = first; s0 < last; s0 += VF_AHEAD) {
+        double w[VF_AHEAD];
+        weights(s0, w);
 #pragma unroll
-      for (int e = 0; e < VF_AHEAD; e++) mine += w[e];
+        for (int e = 0; e < VF_AHEAD; e++) mine += w[e];
+      }
     }
-    share(mine, 0.0);
+    share(mine, 0.0, 0.0);
     // the first block whose running sum passes the point; rounding aside there is one
-    const double total = total_of(all_a);
+    const double total = total_of(0);
     double before = 0.0, base = 0.0;
     int owner = -1, heavy = -1;
 #pragma unroll
     for (int c = 0; c < VF_CLUSTER; c++)
-      if (all_a[c] > 0.0) heavy = c;
+      if (all[0][c] > 0.0) heavy = c;
     const double point = point01 * total;
 #pragma unroll
     for (int c = 0; c < VF_CLUSTER; c++) {
-      if (owner < 0 && (base + all_a[c] > point || c == heavy)) {
+      if (owner < 0 && (base + all[0][c] > point || c == heavy)) {
         owner = c;
         before = base;
       }
-      base += all_a[c];
+      base += all[0][c];
     }
-    if (total > 0.0) {
+    if (total > 1e-280) {
       if (rank != owner) return;
       int ow = -1, hw = -1;
       double wb = before, at = before;
@@ -471,24 +556,52 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
         wb += s_w[0][w];
       }
       if (warp != ow) return;
+      // batch by batch to the one the point falls in, then step by step
       int token = -1, weighted = -1;
       for (int s0 = first; s0 < last && token < 0; s0 += VF_AHEAD) {
-        double w[VF_AHEAD];
+        double w[VF_AHEAD], sum = 0.0;
         weights(s0, w);
+        bool some = false;
 #pragma unroll
         for (int e = 0; e < VF_AHEAD; e++) {
-          double run = w[e];
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(FULL_MASK, run, o);
-            if (lane >= o) run += y;
-          }
-          const unsigned passed = __ballot_sync(FULL_MASK, w[e] > 0.0 && at + run > point);
-          const unsigned some = __ballot_sync(FULL_MASK, w[e] > 0.0);
-          if (passed && token < 0) token = (s0 + e) * 32 + __ffs(passed) - 1;
-          if (some) weighted = (s0 + e) * 32 + 31 - __clz(some);
-          at += __shfl_sync(FULL_MASK, run, 31);
+          sum += w[e];
+          some |= w[e] > 0.0;
         }
+        sum = warp_sum64(sum);
+        if (!__any_sync(FULL_MASK, some)) continue;
+        double step[VF_AHEAD];
+#pragma unroll
+        for (int e = 0; e < VF_AHEAD; e++) {
+          const unsigned some_e = __ballot_sync(FULL_MASK, w[e] > 0.0);
+          if (some_e) weighted = (s0 + e) * 32 + 31 - __clz(some_e);
+        }
+        if (!(at + sum > point)) {
+          at += sum;
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < VF_AHEAD; e++) step[e] = warp_sum64(w[e]);
+        // the step, then the word
+        int es = -1;
+        double mine_w = 0.0;
+#pragma unroll
+        for (int e = 0; e < VF_AHEAD; e++) {
+          if (es < 0 && at + step[e] > point) {
+            es = e;
+            mine_w = w[e];
+          }
+          if (es < 0) at += step[e];
+        }
+        if (es < 0) continue;  // by rounding only: the last word that weighs
+        double run = mine_w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(FULL_MASK, run, o);
+          if (lane >= o) run += y;
+        }
+        const unsigned passed = __ballot_sync(FULL_MASK, mine_w > 0.0 && at + run > point);
+        const unsigned some_s = __ballot_sync(FULL_MASK, mine_w > 0.0);
+        token = (s0 + es) * 32 + (passed ? __ffs(passed) - 1 : 31 - __clz(some_s));
       }
       if (lane == 0) {
         out[j] = token >= 0 ? token : weighted;
@@ -531,8 +644,7 @@ RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_p
       draft_seq < 0 || draft_pos < 0)
     return RLT_ERR_INVALID_ARG;
   if (workspace_bytes < rlt_verify_workspace_bytes(n, k, vocab)) return RLT_ERR_CAPACITY;
-  const double per64 = greedy ? 0.0 : 64.0 * 1.4426950408889634 / (double)temperature;
-  if (!std::isfinite(per64 * 1e38)) return RLT_ERR_INVALID_ARG;
+  const double per = greedy ? 0.0 : 1.4426950408889634 / (double)temperature;
   VerifyArgs A;
   A.target = target;
   A.draft = k > 0 ? draft : nullptr;
@@ -547,8 +659,8 @@ RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_p
   A.k = k;
   A.V = vocab;
   A.chunks = verify_chunks(vocab);
-  A.per64 = per64;
-  A.per1 = (float)(per64 / 64.0);
+  A.per = per;
+  A.per32 = (float)(per < 3e38 ? per : 3e38);  // finite: zero differences stay zero
   A.parts = static_cast<RowPart *>(workspace);
   A.out = tokens;
   A.counts = counts;
