@@ -1,14 +1,12 @@
 // Rows of keys and values into a paged cache (rlt_paged_append) and out of it
 // (rlt_paged_read), as they are or in 8 bits.
 //
-// One thread moves eight elements of a row's head: a 16-byte (bf16) or
-// 32-byte (fp32) piece on the dense side, 8 bytes of e4m3 on the stored one,
-// with the block's largest magnitude found by min(32, DH) / 8 neighbouring
-// lanes. The least e with a <= 448 * 2^e comes from a's own bits: for
-// a = f * 2^x, 1 <= f < 2, it is x - 8, plus one where f > 1.75 (448 = 1.75 *
-// 2^8). x * 2^-e is exact, so the conversion to e4m3 is the only rounding.
-// Bound by memory; a block takes a few neighbouring rows, finds their
-// sequences once, and keeps four pieces a thread in flight.
+// One thread moves a piece of 8 or 16 elements of a row's head, four pieces in
+// flight; in 8 bits the lanes of a block find its largest magnitude a together.
+// The least e with a <= 448 * 2^e comes from a's own bits: for a = f * 2^x,
+// 1 <= f < 2, it is x - 8, plus one where f > 1.75 (448 = 1.75 * 2^8). x * 2^-e is exact, so the conversion to e4m3 is the only rounding.
+// Bound by memory; a block takes a few neighbouring rows and finds their
+// sequences once.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -28,61 +26,68 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// Eight dense elements <-> fp32.
-__device__ __forceinline__ void load8(const float *p, float f[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p);
-  const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// N dense elements <-> fp32 (N a multiple of 8).
+template <int N> __device__ __forceinline__ void load_row(const float *p, float f[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 a = *reinterpret_cast<const float4 *>(p + i);
+    f[i] = a.x; f[i + 1] = a.y; f[i + 2] = a.z; f[i + 3] = a.w;
+  }
 }
-__device__ __forceinline__ void load8(const bf16 *p, float f[8]) { ld16_coherent(p, f); }
-__device__ __forceinline__ void store8(float *p, const float f[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <int N> __device__ __forceinline__ void load_row(const bf16 *p, float f[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) ld16_coherent(p + i, f + i);
 }
-__device__ __forceinline__ void store8(bf16 *p, const float f[8]) {
-  *reinterpret_cast<uint4 *>(p) =
-      make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+template <int N> __device__ __forceinline__ void store_row(float *p, const float f[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4 *>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+}
+template <int N> __device__ __forceinline__ void store_row(bf16 *p, const float f[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    *reinterpret_cast<uint4 *>(p + i) =
+        make_uint4(pack2(f[i], f[i + 1]), pack2(f[i + 2], f[i + 3]), pack2(f[i + 4], f[i + 5]),
+                   pack2(f[i + 6], f[i + 7]));
 }
 
-// Eight elements as e4m3 under a scale shared by LANES neighbouring lanes;
-// returns the scale byte. The lanes of a block are all active.
-template <int LANES>
-__device__ __forceinline__ int quantise8(const float f[8], uint2 &out) {
+// N elements as e4m3 under a scale shared by LANES neighbouring lanes; returns
+// the scale byte. The lanes of a block are all active.
+template <int N, int LANES>
+__device__ __forceinline__ int quantise(const float f[N], uint32_t w[N / 4]) {
   // magnitudes as bits: ordered like the values, infinities and NaN above all
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; i++) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
+  for (int i = 0; i < N; i++) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL_MASK, a, o));
   if (a >= 0x7f800000u) {
-    out = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < N / 4; i++) w[i] = 0;
     return 255;
   }
   // subnormals (exponent field 0) lie far below the least scale
   int e = (int)(a >> 23) - 127 - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = max(e, E4M3_EMIN);
   const float inv = pow2f(-e);
-  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
+  for (int i = 0; i < N / 4; i++) {
     const float2 x = make_float2(f[4 * i] * inv, f[4 * i + 1] * inv);
     const float2 y = make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv);
     w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3) |
            ((uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << 16);
   }
-  out = make_uint2(w[0], w[1]);
   return e + 127;
 }
 
-__device__ __forceinline__ void dequantise8(uint2 v, int sb, float f[8]) {
+template <int N>
+__device__ __forceinline__ void dequantise(const uint32_t w[N / 4], int sb, float f[N]) {
   const float s = __uint_as_float((uint32_t)sb << 23);  // byte 255: infinity, times zero NaN
-  const uint32_t w[2] = {v.x, v.y};
+  const float p = __uint_as_float(0x7b800000u);         // 2^120
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
+  for (int i = 0; i < N / 4; i++) {
     // elements 1, 3 of the word, then 0, 2; raw bf16 bits widened to fp32
     const uint32_t odd = e4m3x2_raw(w[i]), even = e4m3x2_raw(w[i] << 8);
-    const float p = __uint_as_float(0x7b800000u);  // 2^120
     f[4 * i] = __uint_as_float(even << 16) * p * s;
     f[4 * i + 1] = __uint_as_float(odd << 16) * p * s;
     f[4 * i + 2] = __uint_as_float(even & 0xffff0000u) * p * s;
@@ -125,6 +130,12 @@ __device__ void find_rows(const PagedView &C, const RowsView &R, int r0, int nr,
   __syncthreads();
 }
 
+// Elements of a thread's piece: 16 where that is half a block of the scale (a
+// 16-byte access on the stored side), else 8.
+template <int KIND, int DH> constexpr int piece_of() {
+  return KIND == RLT_KV_E4M3 && DH >= 32 ? 16 : 8;
+}
+
 template <typename T, int KIND, int DH, bool WRITE>
 __global__ void __launch_bounds__(PC_THREADS)
     k_paged_rows(PagedView C, RowsView R, T *k, T *v, int64_t ld, int rows_per_block) {
@@ -132,46 +143,98 @@ __global__ void __launch_bounds__(PC_THREADS)
   pdl_wait();
   const int r0 = blockIdx.x * rows_per_block, nr = min(rows_per_block, R.rows - r0);
   find_rows(C, R, r0, nr, place);
-  constexpr int PIECES = DH / 8;                       // of a row's head
-  constexpr int BLOCK = DH < 32 ? DH : 32, LANES = BLOCK / 8;
-  constexpr int SB = DH / BLOCK;                       // scale bytes of a row's head
-  const int per_row = 2 * C.H * PIECES, total = nr * per_row;
-  // every lane of a warp takes every trip: a block's lanes exchange their maxima
-  for (int base = threadIdx.x & ~31; base < total; base += PC_THREADS) {
-    const int i = base + (threadIdx.x & 31);
-    const int row = i / per_row, j = i - row * per_row;
-    const int kv = j / (C.H * PIECES), jj = j - kv * (C.H * PIECES);
-    const int h = jj / PIECES, piece = jj - h * PIECES;
-    const RowPlace p = i < total ? place[row] : RowPlace{-2, 0};
-    T *dense = (kv ? v : k) + (int64_t)(r0 + row) * ld + h * DH + piece * 8;
-    const size_t cell = (((size_t)max(p.page, 0) * C.H + h) * 2 + kv) * C.P + p.slot;
-    if (KIND == RLT_KV_PLAIN) {
-      T *held = reinterpret_cast<T *>(C.pages) + cell * DH + piece * 8;
-      constexpr int N = 8 * sizeof(T) / 16;
-      const uint4 *src = reinterpret_cast<const uint4 *>(WRITE ? dense : held);
-      uint4 *dst = reinterpret_cast<uint4 *>(WRITE ? held : dense);
-      if (p.page >= 0) {
+  constexpr int N = piece_of<KIND, DH>(), PIECES = DH / N;
+  constexpr int BLOCK = DH < 32 ? DH : 32, LANES = BLOCK / N;
+  constexpr int SB = DH / BLOCK;  // scale bytes of a row's head
+  constexpr int U = 4;            // pieces of a thread in flight
+  const int half = C.H * PIECES, per_row = 2 * half;
+  // (row, j): this thread's next piece, j = (kv, head, piece). Every lane of a
+  // warp takes every trip: a block's lanes exchange their maxima.
+  int row = threadIdx.x / per_row, j = threadIdx.x - row * per_row;
+  const int trips = (nr * per_row + PC_THREADS - 1) / PC_THREADS;
+  for (int t = 0; t < trips; t += U) {
+    T *dense[U];
+    size_t cell[U];
+    int page[U], piece[U];
 #pragma unroll
-        for (int x = 0; x < N; x++) dst[x] = src[x];
-      } else if (!WRITE && p.page == -1) {
+    for (int u = 0; u < U; u++) {
+      const RowPlace p = row < nr ? place[row] : RowPlace{-2, 0};
+      const int kv = j >= half, jj = j - kv * half, h = jj / PIECES;
+      piece[u] = jj % PIECES;
+      page[u] = p.page;
+      dense[u] = (kv ? v : k) + (int64_t)(r0 + row) * ld + h * DH + piece[u] * N;
+      cell[u] = (((size_t)max(p.page, 0) * C.H + h) * 2 + kv) * C.P + p.slot;
+      for (j += PC_THREADS; j >= per_row; j -= per_row) row++;
+    }
+    if constexpr (KIND == RLT_KV_PLAIN) {
+      constexpr int Q = N * sizeof(T) / 16;
+      uint4 x[U][Q];
 #pragma unroll
-        for (int x = 0; x < N; x++) dst[x] = make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; u++)
+        if (page[u] >= 0) {
+          const T *held = reinterpret_cast<const T *>(C.pages) + cell[u] * DH + piece[u] * N;
+#pragma unroll
+          for (int y = 0; y < Q; y++)
+            x[u][y] = reinterpret_cast<const uint4 *>(WRITE ? dense[u] : held)[y];
+        } else {
+#pragma unroll
+          for (int y = 0; y < Q; y++) x[u][y] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+      for (int u = 0; u < U; u++)
+        if (page[u] >= (WRITE ? 0 : -1)) {
+          T *held = reinterpret_cast<T *>(C.pages) + cell[u] * DH + piece[u] * N;
+#pragma unroll
+          for (int y = 0; y < Q; y++)
+            reinterpret_cast<uint4 *>(WRITE ? held : dense[u])[y] = x[u][y];
+        }
+    } else if constexpr (WRITE) {
+      float f[U][N];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+#pragma unroll
+        for (int i = 0; i < N; i++) f[u][i] = 0.f;
+        if (page[u] >= 0) load_row<N>(dense[u], f[u]);
       }
-    } else if (WRITE) {
-      float f[8] = {};
-      if (p.page >= 0) load8(dense, f);
-      uint2 q;
-      const int sb = quantise8<LANES>(f, q);
-      if (p.page >= 0) {
-        *reinterpret_cast<uint2 *>(C.pages + cell * DH + piece * 8) = q;
-        if (piece % LANES == 0) C.scales[cell * SB + piece / LANES] = (uint8_t)sb;
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        uint32_t w[N / 4];
+        const int sb = quantise<N, LANES>(f[u], w);
+        if (page[u] >= 0) {
+          uint8_t *dst = C.pages + cell[u] * DH + piece[u] * N;
+          if constexpr (N == 16)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+          if (piece[u] % LANES == 0) C.scales[cell[u] * SB + piece[u] / LANES] = (uint8_t)sb;
+        }
       }
     } else {
-      float f[8] = {};
-      if (p.page >= 0)
-        dequantise8(*reinterpret_cast<const uint2 *>(C.pages + cell * DH + piece * 8),
-                    C.scales[cell * SB + piece / LANES], f);
-      if (p.page >= -1) store8(dense, f);
+      uint32_t w[U][N / 4];
+      int sb[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+#pragma unroll
+        for (int i = 0; i < N / 4; i++) w[u][i] = 0;
+        sb[u] = 127;
+        if (page[u] >= 0) {
+          const uint8_t *src = C.pages + cell[u] * DH + piece[u] * N;
+          if constexpr (N == 16) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(src);
+            w[u][0] = y.x, w[u][1] = y.y, w[u][N / 4 - 2] = y.z, w[u][N / 4 - 1] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2 *>(src);
+            w[u][0] = y.x, w[u][1] = y.y;
+          }
+          sb[u] = C.scales[cell[u] * SB + piece[u] / LANES];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        float f[N];
+        dequantise<N>(w[u], sb[u], f);
+        if (page[u] >= -1) store_row<N>(dense[u], f);
+      }
     }
   }
 }
@@ -182,7 +245,8 @@ cudaError_t run_rows(const rlt_paged_kv *c, const rlt_paged_rows *w, void *k, vo
   const PagedView C = paged_view(c);
   const RowsView R = rows_view(w);
   // about 2048 pieces a block, but blocks for every SM first
-  const int per_row = 2 * c->n_kv_heads * c->head_dim / 8, sms = sm_count();
+  const int piece = c->kind == RLT_KV_E4M3 && c->head_dim >= 32 ? 16 : 8;
+  const int per_row = 2 * c->n_kv_heads * c->head_dim / piece, sms = sm_count();
   int nr = 2048 / per_row;
   if (nr > w->rows / (2 * sms > 0 ? 2 * sms : 1)) nr = w->rows / (2 * sms > 0 ? 2 * sms : 1);
   nr = nr < 1 ? 1 : nr > PC_MAX_ROWS ? PC_MAX_ROWS : nr;

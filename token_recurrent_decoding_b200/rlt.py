@@ -239,40 +239,52 @@ def attend(q, kv, lengths, out, workspace, stream=None):
 
 
 # ------------------------------------------------------------- paged serving
-def _need(ok: bool, what: str):
-    """Arguments the C ABI cannot see (types, shapes, devices of tensors)."""
-    if not ok:
-        raise RLTError(1, what)
+# These calls are made per token, so their checks avoid what is slow in Python:
+# device objects, sizes as tuples, messages that nobody reads.
+_torch = None
 
 
-class _On:
-    """Runs a standalone call on a tensor's device: makes it current and yields the stream's
-    handle (the caller's stream, else the device's current one)."""
-
-    __slots__ = ("torch", "device", "stream", "before")
-
-    def __init__(self, device, stream):
+def _lazy_torch():
+    global _torch
+    if _torch is None:
         import torch
-        self.torch, self.device, self.stream, self.before = torch, device, stream, None
+        _torch = torch
+    return _torch
 
-    def __enter__(self):
-        cuda = self.torch.cuda
-        if self.device.index != cuda.current_device():
-            self.before = cuda.current_device()
-            cuda.set_device(self.device)
-        s = self.stream if self.stream is not None else cuda.current_stream(self.device)
-        return s.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.before is not None:
-            self.torch.cuda.set_device(self.before)
+def _bad(what: str):
+    """An argument the C ABI cannot see (a tensor's type, shape or device)."""
+    raise RLTError(1, what)
 
-    def scratch(self, nbytes):
-        """Workspace of one call, kept from reuse until the call's stream has passed it."""
-        t = self.torch.empty(nbytes, dtype=self.torch.uint8, device=self.device)
-        if self.stream is not None:
-            t.record_stream(self.stream)
-        return t
+
+def _ints(t, dev: int, n: int) -> bool:
+    """Whether t is a contiguous int32 tensor [n] on GPU `dev`."""
+    return (t.dtype is _torch.int32 and t.dim() == 1 and t.size(0) == n and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _launch(dev: int, stream, what: str, fn, *args):
+    """fn(*args, stream handle) with GPU `dev` current, on the caller's stream or the device's."""
+    handle = (stream.cuda_stream if stream is not None
+              else _torch._C._cuda_getCurrentRawStream(dev))
+    now = _torch._C._cuda_getDevice()
+    if now == dev:
+        rc = fn(*args, handle)
+    else:
+        _torch.cuda.set_device(dev)
+        try:
+            rc = fn(*args, handle)
+        finally:
+            _torch.cuda.set_device(now)
+    if rc != RLT_OK:
+        _check(rc, what)
+
+
+def _own(stream, t):
+    """t, made for a call on `stream`, kept from reuse until that stream has passed the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 class PagedKV:
@@ -285,24 +297,26 @@ class PagedKV:
     """
 
     def __init__(self, pages, scales=None, dtype=None):
-        import torch
-        _need(pages.is_cuda and pages.dim() == 5 and pages.shape[2] == 2
-              and pages.is_contiguous(), "PagedKV: pages")
+        torch = _lazy_torch()
+        if not (pages.is_cuda and pages.dim() == 5 and pages.shape[2] == 2
+                and pages.is_contiguous()):
+            _bad("PagedKV: pages")
         e4 = pages.dtype == torch.float8_e4m3fn
         dtype = dtype or (torch.bfloat16 if e4 else pages.dtype)
-        _need(dtype in (torch.float32, torch.bfloat16) and (e4 or dtype == pages.dtype),
-              "PagedKV: dtype")
+        if not (dtype in (torch.float32, torch.bfloat16) and (e4 or dtype == pages.dtype)):
+            _bad("PagedKV: dtype")
         n_pages, heads, _, page, dh = pages.shape
         if e4:
-            _need(scales is not None and scales.dtype == torch.uint8 and scales.is_contiguous()
-                  and scales.device == pages.device
-                  and tuple(scales.shape) == (n_pages, heads, 2, page, dh // min(32, dh)),
-                  "PagedKV: scales")
-        else:
-            _need(scales is None, "PagedKV: scales of a cache that has none")
+            if not (scales is not None and scales.dtype == torch.uint8 and scales.is_contiguous()
+                    and scales.device == pages.device
+                    and tuple(scales.shape) == (n_pages, heads, 2, page, dh // min(32, dh))):
+                _bad("PagedKV: scales")
+        elif scales is not None:
+            _bad("PagedKV: scales of a cache that has none")
         self.pages, self.scales, self.dtype, self.device = pages, scales, dtype, pages.device
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, heads, page, dh
         self.kind = KV_E4M3 if e4 else KV_PLAIN
+        self._dev = pages.get_device()
         self._c = rlt_paged_kv(pages.data_ptr(), scales.data_ptr() if e4 else None, n_pages, page,
                                heads, dh, BF16 if dtype == torch.bfloat16 else 0, self.kind)
         self._ref = C.addressof(self._c)
@@ -311,7 +325,7 @@ class PagedKV:
     def empty(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=None, kind=KV_PLAIN,
               device="cuda"):
         """A new cache of uninitialised pages."""
-        import torch
+        torch = _lazy_torch()
         dtype = dtype or torch.bfloat16
         shape = (n_pages, n_kv_heads, 2, page_size, head_dim)
         if kind == KV_PLAIN:
@@ -321,44 +335,50 @@ class PagedKV:
                    torch.empty(shape[:-1] + (head_dim // block,), dtype=torch.uint8,
                                device=device), dtype)
 
-    def _rows(self, table, cu_rows, kv_len, rows, status, what):
-        import torch
-        i32, dev = torch.int32, self.device
-        n = kv_len.shape[0]
-        _need(table.dtype == i32 and table.dim() == 2 and table.shape[0] == n
-              and table.is_contiguous() and table.device == dev, what + ": page table")
-        _need(cu_rows.dtype == i32 and cu_rows.shape == (n + 1,) and cu_rows.is_contiguous()
-              and cu_rows.device == dev, what + ": cu_rows")
-        _need(kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.is_contiguous()
-              and kv_len.device == dev, what + ": kv_len")
+    def _rows(self, table, cu_rows, kv_len, rows, status):
+        """The C structure, or None where a tensor does not fit."""
+        dev = self._dev
+        n = kv_len.size(0) if kv_len.dim() == 1 else -1
+        if not (_ints(kv_len, dev, n) and _ints(cu_rows, dev, n + 1)
+                and table.dtype is _torch.int32 and table.dim() == 2 and table.size(0) == n
+                and table.is_contiguous() and table.get_device() == dev):
+            return None
         if status is not None:
-            _need(status.dtype == i32 and status.numel() == 1 and status.device == dev,
-                  what + ": status")
+            if not _ints(status, dev, 1):
+                return None
             status = status.data_ptr()
-        return rlt_paged_rows(table.data_ptr(), table.shape[1], cu_rows.data_ptr(),
+        return rlt_paged_rows(table.data_ptr(), table.size(1), cu_rows.data_ptr(),
                               kv_len.data_ptr(), n, rows, status)
 
-    def _dense(self, x, heads, what):
-        """Row stride of a dense buffer [rows][heads][head_dim] whose rows may lie apart."""
-        _need(x.dtype == self.dtype and x.device == self.device and x.dim() == 3
-              and x.shape[1] == heads and x.shape[2] == self.head_dim, what)
-        s = x.stride()
-        _need(s[2] == 1 and (s[1] == self.head_dim or heads == 1), what)
-        return s[0] if x.shape[0] > 1 else max(s[0], heads * self.head_dim)
+    def _stride(self, x, heads):
+        """Row stride of dense rows [rows][heads][head_dim], which may lie apart; -1: they do not fit."""
+        if not (x.dtype is self.dtype and x.dim() == 3 and x.size(1) == heads
+                and x.size(2) == self.head_dim and x.get_device() == self._dev):
+            return -1
+        s0, s1, s2 = x.stride()
+        if s2 != 1 or (s1 != self.head_dim and heads != 1):
+            return -1
+        return s0 if x.size(0) > 1 else max(s0, heads * self.head_dim)
+
+
+_ROWS = "page table int32 [n][width], cu_rows int32 [n + 1], kv_len int32 [n] on the cache's GPU"
 
 
 def _paged_rows_call(fn, what, cache, table, k, v, cu_rows, kv_len, status, stream):
-    ld = cache._dense(k, cache.n_kv_heads, what + ": k")
-    _need(cache._dense(v, cache.n_kv_heads, what + ": v") == ld and v.shape == k.shape,
-          what + ": k and v of one shape and row stride")
-    r = cache._rows(table, cu_rows, kv_len, k.shape[0], status, what)
-    with _On(cache.device, stream) as st:
-        _check(fn(cache._ref, C.addressof(r), k.data_ptr(), v.data_ptr(), ld, st), what)
+    ld = cache._stride(k, cache.n_kv_heads)
+    if ld < 0 or cache._stride(v, cache.n_kv_heads) != ld or v.size(0) != k.size(0):
+        _bad(what + ": k and v [rows][n_kv_heads][head_dim] of the cache's dtype, one row stride")
+    r = cache._rows(table, cu_rows, kv_len, k.size(0), status)
+    if r is None:
+        _bad(what + ": " + _ROWS)
+    _launch(cache._dev, stream, what, fn, cache._ref, C.addressof(r), k.data_ptr(), v.data_ptr(),
+            ld)
 
 
 def paged_append(cache: PagedKV, table, k, v, cu_rows, kv_len, status=None, stream=None):
     """rlt_paged_append: rows of k, v [rows][n_kv_heads][head_dim] into the cache. table int32
-    [n][width], cu_rows int32 [n + 1], kv_len int32 [n] (these rows included), on the GPU."""
+    [n][width], cu_rows int32 [n + 1], kv_len int32 [n] (these rows included), on the GPU;
+    status: None or int32 [1]."""
     _paged_rows_call(_lib().rlt_paged_append, "rlt_paged_append", cache, table, k, v, cu_rows,
                      kv_len, status, stream)
 
@@ -379,32 +399,34 @@ def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_l
                  lse=None, window: int = 0, workspace=None, status=None, stream=None):
     """rlt_attend_paged: q [rows][n_heads][head_dim] over the cache -> out (allocated where None;
     rows behind the last sequence are not written). lse: None or float32 [rows][n_heads]."""
-    import torch
-    what = "rlt_attend_paged"
-    _need(q.dim() == 3, what + ": q")
-    rows, heads = q.shape[0], q.shape[1]
-    ldq = cache._dense(q, heads, what + ": q")
-    on = _On(cache.device, stream)
+    what, dev, torch = "rlt_attend_paged", cache._dev, _torch
+    rows, heads = (q.size(0), q.size(1)) if q.dim() == 3 else (0, 0)
+    ldq = cache._stride(q, heads)
+    if ldq < 0:
+        _bad(what + ": q [rows][n_heads][head_dim] of the cache's dtype")
     if out is None:
-        out = torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
-        if stream is not None:
-            out.record_stream(stream)
-    ldo = cache._dense(out, heads, what + ": out")
-    _need(out.shape == q.shape, what + ": out")
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.shape == (rows, heads) and lse.is_contiguous()
-              and lse.device == cache.device, what + ": lse")
-    r = cache._rows(table, cu_rows, kv_len, rows, status, what)
+        out = _own(stream, torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype,
+                                       device=cache.device))
+    ldo = cache._stride(out, heads)
+    if ldo < 0 or out.size(0) != rows:
+        _bad(what + ": out of q's shape and dtype")
+    if lse is not None and not (lse.dtype is torch.float32 and lse.dim() == 2
+                                and lse.size(0) == rows and lse.size(1) == heads
+                                and lse.is_contiguous() and lse.get_device() == dev):
+        _bad(what + ": lse float32 [rows][n_heads]")
+    r = cache._rows(table, cu_rows, kv_len, rows, status)
+    if r is None:
+        _bad(what + ": " + _ROWS)
     if workspace is None:
-        workspace = on.scratch(attend_paged_workspace_bytes(cache, r.n, heads, rows, max_rows,
-                                                            max_len))
-    _need(workspace.device == cache.device and workspace.dtype == torch.uint8
-          and workspace.is_contiguous(), what + ": workspace")
-    with on as st:
-        _check(_lib().rlt_attend_paged(
-            cache._ref, C.addressof(r), q.data_ptr(), ldq, heads, max_rows, max_len, window,
-            out.data_ptr(), ldo, lse.data_ptr() if lse is not None else None,
-            workspace.data_ptr(), workspace.numel(), st), what)
+        workspace = _own(stream, torch.empty(
+            attend_paged_workspace_bytes(cache, r.n, heads, rows, max_rows, max_len),
+            dtype=torch.uint8, device=cache.device))
+    elif not (workspace.dtype is torch.uint8 and workspace.is_contiguous()
+              and workspace.get_device() == dev):
+        _bad(what + ": workspace uint8 on the cache's GPU")
+    _launch(dev, stream, what, _lib().rlt_attend_paged, cache._ref, C.addressof(r), q.data_ptr(),
+            ldq, heads, max_rows, max_len, window, out.data_ptr(), ldo,
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -417,55 +439,52 @@ def verify(target, draft, draft_tokens, temperature: float, uniforms=None, draft
     """rlt_verify: target float32 [n][k + 1][V] and draft float32 [n][k][V] (or None) in any strides
     of their first two dimensions, draft_tokens int32 [n][k], uniforms float32 [n][k + 1],
     draft_lengths int32 [n] or None -> (tokens int32 [n][k + 1], counts int32 [n])."""
-    import torch
-    what, dev = "rlt_verify", target.device
-    _need(target.is_cuda and target.dtype == torch.float32 and target.dim() == 3
-          and (target.stride(2) == 1 or target.shape[2] == 1), what + ": target")
-    n, k, V = target.shape[0], target.shape[1] - 1, target.shape[2]
-    ts = target.stride()
-    ds = (0, 0)
+    torch = _lazy_torch()
+    what, dev = "rlt_verify", target.get_device()
+    if not (target.dtype is torch.float32 and target.dim() == 3 and dev >= 0):
+        _bad(what + ": target float32 [n][k + 1][V] on a GPU")
+    n, k, V = target.size(0), target.size(1) - 1, target.size(2)
+    t0, t1, t2 = target.stride()
+    d0 = d1 = 0
+    if t2 != 1 and V != 1:
+        _bad(what + ": target's last dimension contiguous")
     if draft is not None:
-        _need(draft.dtype == torch.float32 and draft.shape == (n, k, V) and draft.device == dev
-              and (draft.stride(2) == 1 or V == 1), what + ": draft")
-        ds = draft.stride()
-    _need(draft_tokens is None and k == 0 or draft_tokens is not None
-          and draft_tokens.dtype == torch.int32 and draft_tokens.shape == (n, k)
-          and draft_tokens.is_contiguous() and draft_tokens.device == dev,
-          what + ": draft_tokens")
-    _need(uniforms is None and temperature == 0 or uniforms is not None
-          and uniforms.dtype == torch.float32 and uniforms.shape == (n, k + 1)
-          and uniforms.is_contiguous() and uniforms.device == dev, what + ": uniforms")
-    if draft_lengths is not None:
-        _need(draft_lengths.dtype == torch.int32 and draft_lengths.shape == (n,)
-              and draft_lengths.is_contiguous() and draft_lengths.device == dev,
-              what + ": draft_lengths")
-    on = _On(dev, stream)
-    made = []
+        d0, d1, d2 = draft.stride() if draft.dim() == 3 else (0, 0, 0)
+        if not (draft.dtype is torch.float32 and draft.dim() == 3 and draft.size(0) == n
+                and draft.size(1) == k and draft.size(2) == V and draft.get_device() == dev
+                and (d2 == 1 or V == 1)):
+            _bad(what + ": draft float32 [n][k][V], its last dimension contiguous")
+
+    def fits(t, dtype, cols):
+        return (t.dtype is dtype and t.dim() == 2 and t.size(0) == n and t.size(1) == cols
+                and t.is_contiguous() and t.get_device() == dev)
+
+    if k and (draft_tokens is None or not fits(draft_tokens, torch.int32, k)):
+        _bad(what + ": draft_tokens int32 [n][k]")
+    if temperature != 0 and (uniforms is None or not fits(uniforms, torch.float32, k + 1)):
+        _bad(what + ": uniforms float32 [n][k + 1]")
+    if draft_lengths is not None and not _ints(draft_lengths, dev, n):
+        _bad(what + ": draft_lengths int32 [n]")
     if tokens is None:
-        tokens = torch.empty((n, k + 1), dtype=torch.int32, device=dev)
-        made.append(tokens)
+        tokens = _own(stream, torch.empty((n, k + 1), dtype=torch.int32, device=target.device))
+    elif not fits(tokens, torch.int32, k + 1):
+        _bad(what + ": tokens int32 [n][k + 1]")
     if counts is None:
-        counts = torch.empty(n, dtype=torch.int32, device=dev)
-        made.append(counts)
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
-    _need(tokens.dtype == torch.int32 and tokens.shape == (n, k + 1) and tokens.is_contiguous()
-          and tokens.device == dev, what + ": tokens")
-    _need(counts.dtype == torch.int32 and counts.shape == (n,) and counts.is_contiguous()
-          and counts.device == dev, what + ": counts")
+        counts = _own(stream, torch.empty(n, dtype=torch.int32, device=target.device))
+    elif not _ints(counts, dev, n):
+        _bad(what + ": counts int32 [n]")
     if workspace is None:
-        workspace = on.scratch(verify_workspace_bytes(n, k, V))
-    _need(workspace.device == dev and workspace.dtype == torch.uint8
-          and workspace.is_contiguous(), what + ": workspace")
-    with on as st:
-        _check(_lib().rlt_verify(
-            target.data_ptr(), ts[0], ts[1], draft.data_ptr() if draft is not None else None,
-            ds[0], ds[1], draft_tokens.data_ptr() if k else None,
-            draft_lengths.data_ptr() if draft_lengths is not None else None, n, k, V,
-            float(temperature), uniforms.data_ptr() if uniforms is not None else None,
-            tokens.data_ptr(), counts.data_ptr(), workspace.data_ptr(), workspace.numel(), st),
-            what)
+        workspace = _own(stream, torch.empty(verify_workspace_bytes(n, k, V), dtype=torch.uint8,
+                                             device=target.device))
+    elif not (workspace.dtype is torch.uint8 and workspace.is_contiguous()
+              and workspace.get_device() == dev):
+        _bad(what + ": workspace uint8 on the logits' GPU")
+    _launch(dev, stream, what, _lib().rlt_verify, target.data_ptr(), t0, t1,
+            None if draft is None else draft.data_ptr(), d0, d1,
+            draft_tokens.data_ptr() if k else None,
+            None if draft_lengths is None else draft_lengths.data_ptr(), n, k, V, temperature,
+            None if temperature == 0 or uniforms is None else uniforms.data_ptr(),
+            tokens.data_ptr(), counts.data_ptr(), workspace.data_ptr(), workspace.numel())
     return tokens, counts
 
 
