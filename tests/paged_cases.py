@@ -46,7 +46,7 @@ class Case:
     """A cache with random contents, its page table, and a chunk of rows per sequence."""
 
     def __init__(self, rows, lens, H=2, dh=64, page=16, dtype=BF16, e4=False, seed=0, stale=None,
-                 pad=0):
+                 pad=0, value_scale=1.0):
         g = torch.Generator().manual_seed(seed)
         self.g, self.rows, self.lens = g, list(rows), list(lens)
         self.H, self.dh, self.page, self.dtype, self.e4 = H, dh, page, dtype, e4
@@ -74,6 +74,7 @@ class Case:
         for b, L in enumerate(lens):
             x = torch.randn((L, H, 2, dh), generator=g, dtype=torch.float64)
             x[:, :, 0] *= 1.5
+            x[::2, :, 1] *= value_scale  # every other position
             x = x.to(dtype).double()
             if e4:
                 v, s = quantised(x.numpy())

@@ -200,6 +200,25 @@ def test_sharp_scores_and_long_sequences(kind):
     _check(c, 2, scale=6.0)
 
 
+@pytest.mark.parametrize("value_scale", [1e6, 1e30, 1e-30])
+@pytest.mark.parametrize("dtype,m,dh", [(BF16, 2, 128), (BF16, 60, 128), (F32, 3, 64),
+                                        (BF16, 2, 32)])
+def test_scales_far_from_one(value_scale, dtype, m, dh):
+    c = Case([m, 1], [90 + m, 33], H=2, dh=dh, page=16, dtype=dtype, e4=True, seed=11,
+             value_scale=value_scale).device()
+    _check(c, 2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16e4"])
+@pytest.mark.parametrize("dh,m,lens", [(128, 40, [9000, 700]), (64, 300, [9100, 4300]),
+                                       (128, 33, [128, 40])])
+def test_long_sequences_and_wide_tiles(kind, dh, m, lens):
+    """Split ranges, streams of key tiles (an odd number of them, one of them) and tiles whose
+    second half has few rows or none."""
+    c = Case([m, 35], lens, H=1, dh=dh, page=128, e4=kind.endswith("e4"), seed=12).device()
+    _check(c, 1, window=0 if dh == 128 else 8000)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32", "bf16e4"])
 @pytest.mark.parametrize("m", [3, 90])
 def test_what_lies_in_unseen_places_does_not_matter(kind, m):

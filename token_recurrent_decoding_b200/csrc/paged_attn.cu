@@ -1,4 +1,5 @@
 // rlt_attend_paged: checks, the choice of kernels, launches.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -8,18 +9,12 @@
 namespace rlt {
 namespace {
 
-bool attn_shape_ok(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows, int max_len) {
-  return paged_shape_status(c) == RLT_OK && n >= 1 && n <= RLT_PAGED_MAX_SEQS && n_heads >= 1 &&
-         n_heads <= 1024 && n_heads % c->n_kv_heads == 0 && rows >= 0 && max_rows >= 0 &&
-         max_len >= 0 && max_len <= (1 << 28) && (int64_t)rows * n_heads <= (1 << 28) &&
-         (int64_t)max_rows * n_heads <= (1 << 28);
+bool wide_kernel(const rlt_paged_kv *c) {
+  return c->dtype == RLT_BF16 && (c->head_dim == 64 || c->head_dim == 128);
 }
-
-// Stacked rows per kv head from which a sequence goes to the tcgen05 kernel
-// (bf16 rows, head sizes 64 and 128).
-constexpr int WIDE_FROM = 33;
-int wide_from(const rlt_paged_kv *c) {
-  return c->dtype == RLT_BF16 && (c->head_dim == 64 || c->head_dim == 128) ? WIDE_FROM : 1 << 30;
+// Whether a sequence within this bound may go to k_pattn_wide.
+bool may_be_wide(const rlt_paged_kv *c, int n_heads, int max_rows) {
+  return wide_kernel(c) && (int64_t)max_rows * (n_heads / c->n_kv_heads) >= PA_WIDE_FROM;
 }
 
 int64_t most_splits(int max_len, int min_keys) {
@@ -27,24 +22,44 @@ int64_t most_splits(int max_len, int min_keys) {
   return n < PA_MAX_SPLITS ? n : PA_MAX_SPLITS;
 }
 
-// Partial rows the split rule can make: a sequence of m rows makes at most
-// m * heads * splits, with splits below units aimed at / own units + 1 and own
-// units at least m * heads / rows of a unit; only sequences the kernel takes
-// count.
+// Partial rows the split rule can make, at most. k_pattn: a sequence of m rows
+// makes m * heads * splits, with splits below units aimed at / own units + 1 and
+// own units at least m * heads / rows of a unit. k_pattn_wide: the same for
+// tiles; streams: two slices a range of at most PA_STREAM_ROWS rows a kv head.
 int64_t partial_rows(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows,
                      int max_len) {
-  const int group = n_heads / c->n_kv_heads, wide = wide_from(c);
-  const int64_t cells = (int64_t)rows * n_heads;
-  int64_t a = most_splits(max_len, PA_MIN_KEYS) > 1 ? (int64_t)n * PA_SPLIT_UNITS * PA_UNIT_ROWS : 0;
-  int64_t b = 0;
-  if ((int64_t)max_rows * group >= wide && most_splits(max_len, PA_WIDE_KEYS) > 1) {
-    int64_t seqs = (int64_t)rows * group / wide;
-    if (seqs > n) seqs = n;
-    b = seqs * PA_WIDE_UNITS * PA_WIDE_ROWS;
+  const int64_t cells = (int64_t)rows * n_heads, narrow = most_splits(max_len, PA_MIN_KEYS);
+  int64_t most = narrow > 1 ? (int64_t)n * PA_SPLIT_UNITS * PA_UNIT_ROWS + cells : 0;
+  if (most > narrow * cells) most = narrow * cells;
+  if (wide_kernel(c) && most > 0) {
+    // only few rows are left to k_pattn
+    const int64_t few = (int64_t)n * PA_WIDE_FROM * c->n_kv_heads * narrow;
+    if (most > few) most = few;
   }
-  if (a + b == 0) return 0;
-  const int64_t all = most_splits(max_len, PA_MIN_KEYS) * cells;
-  return a + b + cells < all ? a + b + cells : all;
+  if (may_be_wide(c, n_heads, max_rows)) {
+    const int64_t wide = most_splits(max_len, PA_WIDE_KEYS),
+                  streams = 2 * most_splits(max_len, PA_STREAM_KEYS);
+    int64_t a = 0, b = streams * cells;
+    if (wide > 1) {
+      // (sequences of more than PA_STREAM_ROWS stacked rows)
+      int64_t seqs = (int64_t)rows * (n_heads / c->n_kv_heads) / PA_STREAM_ROWS;
+      if (seqs > n) seqs = n;
+      a = seqs * PA_WIDE_UNITS * PA_WIDE_ROWS + cells;
+      if (a > wide * cells) a = wide * cells;
+    }
+    const int64_t few = (int64_t)n * PA_STREAM_ROWS * c->n_kv_heads * streams;
+    if (b > few) b = few;
+    most += a + b;
+  }
+  return most;
+}
+
+bool attn_shape_ok(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows, int max_len) {
+  return paged_shape_status(c) == RLT_OK && n >= 1 && n <= RLT_PAGED_MAX_SEQS && n_heads >= 1 &&
+         n_heads <= 1024 && n_heads % c->n_kv_heads == 0 && rows >= 0 && max_rows >= 0 &&
+         max_len >= 0 && max_len <= (1 << 28) && (int64_t)rows * n_heads <= (1 << 28) &&
+         (int64_t)max_rows * n_heads <= (1 << 28) &&
+         partial_rows(c, n, n_heads, rows, max_rows, max_len) <= (1 << 30);
 }
 
 size_t workspace_bytes_of(int dh, int64_t part_rows) {
@@ -57,7 +72,7 @@ cudaError_t launch_warp_kernel(const AttnArgs &A, int sms, cudaStream_t st) {
   using Cfg = PaCfg<KIND, DH, MT>;
   const cudaError_t e = ensure_smem_limit(k_pattn<KIND, DH, MT>, Cfg::bytes(RLT_PAGED_MAX_SEQS));
   if (e != cudaSuccess) return e;
-  const int smem = Cfg::bytes(A.R.n), per_sm = smem <= 113 * 1024 ? 2 : 1;
+  const int smem = Cfg::bytes(A.R.n), per_sm = std::max(1, std::min(Cfg::CTAS, 227 * 1024 / (smem + 1024)));
   // items of the batch, at most: a grid no larger than its work
   const int64_t tiles = (int64_t)A.R.rows * A.group / Cfg::RT + A.R.n;
   int64_t items = tiles * A.C.H * PA_MAX_SPLITS;
@@ -158,7 +173,7 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
   A.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->head_dim));
   A.part = static_cast<float *>(workspace);
   A.part_rows = (int)parts;
-  A.wide_from = wide_from(c);
+  A.wide = wide_kernel(c);
   A.follows = 1;
   cudaStream_t st = (cudaStream_t)stream;
   const int sms = sm_count(), dh = c->head_dim;
@@ -169,7 +184,7 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
     e = e4 ? launch_attn<PA_E4M3>(A, dh, sms, st) : launch_attn<PA_BF16>(A, dh, sms, st);
   else
     e = e4 ? launch_attn<PA_E4M3_F32>(A, dh, sms, st) : launch_attn<PA_F32>(A, dh, sms, st);
-  if (e == cudaSuccess && (int64_t)max_rows * A.group >= A.wide_from)
+  if (e == cudaSuccess && may_be_wide(c, n_heads, max_rows))
     e = launch_wide(A, e4, dh, sms, st);
   if (e == cudaSuccess && parts > 0)
     e = c->dtype == RLT_BF16 ? launch_merge<bf16>(A, dh, sms, st)

@@ -40,38 +40,57 @@ constexpr int PA_TK = 16;            // keys of a tile
 constexpr int PA_UNIT_ROWS = 32;     // rows of a unit in the split rule
 constexpr int PA_SPLIT_UNITS = 256;  // units x splits aimed at per sequence
 constexpr int PA_MAX_SPLITS = 16;
-constexpr int PA_MIN_KEYS = 256;     // least keys of a split
+constexpr int PA_MIN_KEYS = 256;     // least keys of a split ..
+constexpr int PA_ROW_KEYS = 32;      // .. and for each row of a unit
 // The same of sequences that go to the tcgen05 kernel: tiles of 256 rows, one
 // CTA per SM, splits long enough that writing O in fp32 stays below a tenth.
+// Of sequences of at most PA_STREAM_ROWS rows both halves of a CTA take the same
+// rows and every other key tile (two streams, two slices of the split).
+constexpr int PA_WIDE_FROM = 33;     // rows from which a sequence goes there
 constexpr int PA_WIDE_ROWS = 256;
 constexpr int PA_WIDE_UNITS = 148;
 constexpr int PA_WIDE_KEYS = 4096;
+constexpr int PA_STREAM_ROWS = 128;
+constexpr int PA_STREAM_KEYS = 2048;
 
 // How one sequence is cut, from its own rows and length only.
 struct SeqCut {
-  int m, first;     // rows, position of the first
-  int k_lo, k_hi;   // keys any of its rows sees; k_lo is a multiple of 16
-  int splits, keys; // ranges and keys of a range (a multiple of 16)
+  int m, first;      // rows, position of the first
+  int k_lo, k_hi;    // keys any of its rows sees; k_lo is a multiple of 16
+  int ranges, keys;  // key ranges and keys of one (a multiple of 16)
+  int splits;        // slices its results come in: ranges, or two of each
+  bool wide, streams;
 };
 
 __device__ __host__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_heads, int window,
-                                          bool wide) {
+                                          bool wide_kernel) {
   SeqCut s;
   s.m = m;
   s.first = len - m;
   s.k_hi = max(len, 0);
   const int lo = window > 0 ? max(0, max(s.first, 0) - window + 1) : 0;
   s.k_lo = min(lo, s.k_hi) & ~(PA_TK - 1);
-  const int span = s.k_hi - s.k_lo;
-  const int units = max(1, kv_heads * ceil_div(m * group, wide ? PA_WIDE_ROWS : PA_UNIT_ROWS));
-  // (a wide unit fills an SM: rounded down, two thirds of a second wave cost more than idle SMs)
-  int n = min(min(PA_MAX_SPLITS, wide ? PA_WIDE_UNITS / units : ceil_div(PA_SPLIT_UNITS, units)),
-              ceil_div(span, wide ? PA_WIDE_KEYS : PA_MIN_KEYS));
-  n = max(n, 1);
+  const int span = s.k_hi - s.k_lo, rows = m * group;
+  s.wide = wide_kernel && rows >= PA_WIDE_FROM;
+  s.streams = s.wide && rows <= PA_STREAM_ROWS;
+  int n;
+  if (s.streams) {
+    n = span / PA_STREAM_KEYS;
+  } else if (s.wide) {
+    // a unit fills an SM: rounded down, as a second wave costs more than idle SMs
+    n = min(PA_WIDE_UNITS / (kv_heads * ceil_div(rows, PA_WIDE_ROWS)), ceil_div(span, PA_WIDE_KEYS));
+  } else {
+    const int units = max(1, kv_heads * ceil_div(rows, PA_UNIT_ROWS));
+    // (writing and joining a slice stays below a tenth of reading its keys)
+    n = min(ceil_div(PA_SPLIT_UNITS, units),
+            ceil_div(span, max(PA_MIN_KEYS, PA_ROW_KEYS * min(rows, PA_UNIT_ROWS))));
+  }
+  n = max(1, min(n, PA_MAX_SPLITS));
   s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);
-  s.splits = max(1, ceil_div(span, s.keys));
+  s.ranges = max(1, ceil_div(span, s.keys));
+  s.splits = s.streams ? 2 * s.ranges : s.ranges;
   return s;
 }
 
@@ -87,7 +106,7 @@ struct AttnArgs {
   float scale_log2;  // log2(e) / sqrt(head_dim)
   float *part;       // [part_rows][DH + 2]: O (not divided), maximum (base 2), sum
   int part_rows;
-  int wide_from;     // sequences with this many stacked rows per kv head go to k_pattn_wide
+  int wide;          // whether k_pattn_wide takes part (its types and head sizes)
   int follows;       // k_pattn_wide: k_pattn of the same call runs before it
 };
 
@@ -101,7 +120,7 @@ __device__ __forceinline__ SeqCut cut_of(const AttnArgs &A, int b, int &row0, in
     const int len = A.R.len[b];
     if (hi - lo <= A.max_rows && len >= 0 && len <= A.max_len) {
       row0 = lo;
-      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, (hi - lo) * A.group >= A.wide_from);
+      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, A.wide);
     }
     flag_rows(A.R, RLT_PAGED_BAD_ROWS);
   }
@@ -189,7 +208,9 @@ template <int KIND, int DH, int MT> struct PaCfg {
   static constexpr int SB = !E4 ? 0 : DH < 32 ? 1 : DH / 32;  // scale bytes of a row
   static constexpr int KV = PA_TK * RB;
   static constexpr int STAGE = 2 * KV + (E4 ? 2 * PA_TK * SB : 0);
-  static constexpr int STAGES = KIND == PA_F32 && DH == 128 ? 2 : 3;
+  // CTAs of an SM the registers are cut for, and stages that fit as often
+  static constexpr int CTAS = MT == 1 && QP == 1 ? 3 : 2;
+  static constexpr int STAGES = DH == 128 && (KIND == PA_F32 || (KIND == PA_BF16 && MT == 1)) ? 2 : 3;
   static constexpr int RT = 16 * MT;
   static constexpr int RING = 4 * STAGES * STAGE;
   static constexpr int JOIN = 4 * RT * DH * 4;  // O of the four warps, over the ring
@@ -276,6 +297,11 @@ __device__ __forceinline__ void mma_parts(float c[4], const uint32_t a[][4], con
     }
 }
 
+// Two codes as bf16 values: scale2 is their scales, or with TWO unset 2^120 of them.
+template <bool TWO> __device__ __forceinline__ uint32_t pa_codes(uint32_t w, uint32_t scale2) {
+  return TWO ? e4m3x2_value(w, scale2) : bmul2(e4m3x2_raw(w), scale2);
+}
+
 // Head entry i = 0..3 of lane t's four in product step ks (the two of the
 // operand's low half, then the two of its high half).
 template <int KIND, int DH> __device__ __forceinline__ int head_order(int ks, int t, int i) {
@@ -291,7 +317,7 @@ template <int KIND, int DH> __device__ __forceinline__ int col_of(int j, int t, 
 }
 
 template <int KIND, int DH, int MT>
-__global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
+__global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn(const AttnArgs A) {
   using Cfg = PaCfg<KIND, DH, MT>;
   using TQ = typename std::conditional<Cfg::QP == 3, float, bf16>::type;
   constexpr int RB = Cfg::RB, CPR = Cfg::CPR, SB = Cfg::SB, QP = Cfg::QP, KP = Cfg::KP;
@@ -306,7 +332,7 @@ __global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
   pdl_wait();
   pdl_trigger();
   scan_seqs<PA_THREADS>(A, items, parts, [&](const SeqCut &s) {
-    return s.m * A.group < A.wide_from ? A.C.H * s.splits * ceil_div(s.m * A.group, RT) : 0;
+    return s.wide ? 0 : A.C.H * s.splits * ceil_div(s.m * A.group, RT);
   });
   const int total = items[A.R.n];
 
@@ -368,46 +394,54 @@ __global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
       l[mt][0] = l[mt][1] = 0.f;
     }
 
-    // lane i holds the page of the warp's tile i of the current 32
-    int pages = -1;
+    // lane i holds the row of the cache's key plane where the warp's tile i of
+    // the current 32 begins (as many 16-byte rows as 36 bits reach: any GPU's
+    // memory), or NO_PAGE
+    constexpr int64_t NO_PAGE = -1;
+    int64_t cells = NO_PAGE;
     uint32_t absent = 0;  // tiles of the last 32 whose page does not exist
+    const uint8_t *lane_src = A.C.pages + lane * 16;
+    const size_t plane = (size_t)A.C.P * RB;
     auto load = [&](int i) {
       if ((i & 31) == 0) {
-        const int tile = t0 + warp + 4 * (i + lane);
-        pages = -1;
+        const int key = (t0 + warp + 4 * (i + lane)) * PA_TK;
+        cells = NO_PAGE;
         if (i + lane < my) {
-          const int idx = tile * PA_TK / A.C.P;
-          if (idx < A.R.width) pages = A.R.table[(size_t)b * A.R.width + idx];
-          if (pages < 0 || pages >= A.C.n_pages) {
-            pages = -1;
+          const int idx = key / A.C.P;
+          int pid = -1;
+          if (idx < A.R.width) pid = A.R.table[(size_t)b * A.R.width + idx];
+          if (pid >= 0 && pid < A.C.n_pages)
+            cells = ((int64_t)pid * A.C.H + kvh) * 2 * A.C.P + (key - idx * A.C.P);
+          else
             flag_rows(A.R, RLT_PAGED_BAD_PAGE);
-          }
         }
       }
-      const int pid = __shfl_sync(FULL_MASK, pages, i & 31);
-      const int key0 = (t0 + warp + 4 * i) * PA_TK;
-      absent = (absent & ~(1u << (i & 31))) | (uint32_t)(pid < 0) << (i & 31);
-      const size_t cell =
-          ((size_t)max(pid, 0) * A.C.H + kvh) * 2 * A.C.P + (pid < 0 ? 0 : key0 % A.C.P);
-      const uint8_t *ksrc = A.C.pages + cell * RB, *vsrc = ksrc + (size_t)A.C.P * RB;
+      const int64_t cell = __shfl_sync(FULL_MASK, cells, i & 31);
+      const bool there = cell != NO_PAGE;
+      const int left = there ? S.k_hi - (t0 + warp + 4 * i) * PA_TK : 0;  // keys of the tile
+      absent = (absent & ~(1u << (i & 31))) | (uint32_t)!there << (i & 31);
+      const uint8_t *ksrc = lane_src + (there ? cell * RB : 0), *vsrc = ksrc + plane;
       const uint32_t dst = ring_u + (i % Cfg::STAGES) * Cfg::STAGE;
-#pragma unroll
-      for (int x = 0; x < (RB + 31) / 32; x++) {
+      // rows behind the sequence hold anything: read as zeros
+      auto copy = [&](int x, int bytes) {
         const int c = x * 32 + lane;
-        if (RB >= 32 || c < RB) {
-          const int r = c / CPR, cc = c % CPR;
-          // rows behind the sequence hold anything: read as zeros
-          const int bytes = pid >= 0 && key0 + r < S.k_hi ? 16 : 0;
-          const uint32_t at = dst + pa_piece<Cfg>(r, cc) * 16;
-          cp_async16(at, ksrc + c * 16, bytes);
-          cp_async16(at + Cfg::KV, vsrc + c * 16, bytes);
-        }
+        const uint32_t at = dst + pa_piece<Cfg>(c / CPR, c % CPR) * 16;
+        cp_async16(at, ksrc + x * 512, bytes);
+        cp_async16(at + Cfg::KV, vsrc + x * 512, bytes);
+      };
+      if (left >= PA_TK && RB >= 32) {
+#pragma unroll
+        for (int x = 0; x < (RB + 31) / 32; x++) copy(x, 16);
+      } else {
+#pragma unroll
+        for (int x = 0; x < (RB + 31) / 32; x++)
+          if (RB >= 32 || lane < RB) copy(x, (x * 32 + lane) / CPR < left ? 16 : 0);
       }
       if constexpr (Cfg::E4) {
         if (lane < 2 * SB) {
           const int kv = lane / SB, c = lane % SB;
-          const uint8_t *src = A.C.scales + (cell + (kv ? A.C.P : 0)) * SB + c * 16;
-          cp_async16(dst + 2 * Cfg::KV + lane * 16, src, pid >= 0 ? 16 : 0);
+          const uint8_t *src = A.C.scales + (there ? (cell + (kv ? A.C.P : 0)) * SB + c * 16 : 0);
+          cp_async16(dst + 2 * Cfg::KV + lane * 16, src, there ? 16 : 0);
         }
       }
     };
@@ -464,6 +498,17 @@ __global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
         __syncwarp();
       }
 
+      // 8 bits: one multiplication by 2^(120 + e) where that is finite for
+      // every scale of the tile (e <= 7, magnitudes up to 448 * 128), else two
+      bool large = false;
+      if constexpr (Cfg::E4) {
+        constexpr int WORDS = 2 * PA_TK * SB / 4;
+        uint32_t over = 0;
+        for (int x = lane; x < WORDS; x += 32)
+          over |= __vcmpgtu4(reinterpret_cast<const uint32_t *>(sck)[x], 0x86868686u);
+        large = __any_sync(FULL_MASK, over != 0);
+      }
+
       // S = Q K^T: two column tiles of 8 keys
       float s[MT][2][4];
 #pragma unroll
@@ -498,35 +543,41 @@ __global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
             for (int mt = 0; mt < MT; mt++) mma_parts<QP, KP>(s[mt][n], qf[mt][ks], b0, b1);
           }
       } else {
-        constexpr int GK = KS < 4 ? KS : 4;  // steps served by one piece of 4 * GK codes
-#pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-          for (int kg = 0; kg < KS / GK; kg++) {
-            const int row = n * 8 + g, byte = kg * GK * 16 + t * GK * 4;
-            const uint8_t *src = st + pa_piece<Cfg>(row, byte / 16) * 16 + byte % 16;
-            uint32_t w[GK];
-            if (GK == 4) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(src);
-              w[0] = x.x, w[GK > 1 ? 1 : 0] = x.y, w[GK > 2 ? 2 : 0] = x.z, w[GK > 3 ? 3 : 0] = x.w;
-              w[0] = x.x;
-            } else if (GK == 2) {
-              const uint2 x = *reinterpret_cast<const uint2 *>(src);
-              w[GK > 1 ? 1 : 0] = x.y;
-              w[0] = x.x;
-            } else {
-              w[0] = *reinterpret_cast<const uint32_t *>(src);
+        auto products = [&](auto two) {
+          constexpr int GK = KS < 4 ? KS : 4;  // steps served by one piece of 4 * GK codes
+  #pragma unroll
+          for (int n = 0; n < 2; n++)
+  #pragma unroll
+            for (int kg = 0; kg < KS / GK; kg++) {
+              const int row = n * 8 + g, byte = kg * GK * 16 + t * GK * 4;
+              const uint8_t *src = st + pa_piece<Cfg>(row, byte / 16) * 16 + byte % 16;
+              uint32_t w[GK];
+              if (GK == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                w[0] = x.x, w[GK > 1 ? 1 : 0] = x.y, w[GK > 2 ? 2 : 0] = x.z, w[GK > 3 ? 3 : 0] = x.w;
+                w[0] = x.x;
+              } else if (GK == 2) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                w[GK > 1 ? 1 : 0] = x.y;
+                w[0] = x.x;
+              } else {
+                w[0] = *reinterpret_cast<const uint32_t *>(src);
+              }
+              const uint32_t sb = sck[row * SB + (SB > 1 ? byte / 32 : 0)] + (decltype(two)::value ? 0 : 120);
+              const uint32_t sc = scale_pair(sb, sb);
+  #pragma unroll
+              for (int x = 0; x < GK; x++) {
+                const uint32_t b0 = pa_codes<decltype(two)::value>(w[x] << 8, sc), b1 = pa_codes<decltype(two)::value>(w[x], sc);
+  #pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+                  mma_parts<QP, 1>(s[mt][n], qf[mt][kg * GK + x], &b0, &b1);
+              }
             }
-            const uint32_t sb = sck[row * SB + (SB > 1 ? byte / 32 : 0)];
-            const uint32_t sc = scale_pair(sb, sb);
-#pragma unroll
-            for (int x = 0; x < GK; x++) {
-              const uint32_t b0 = e4m3x2_value(w[x] << 8, sc), b1 = e4m3x2_value(w[x], sc);
-#pragma unroll
-              for (int mt = 0; mt < MT; mt++)
-                mma_parts<QP, 1>(s[mt][n], qf[mt][kg * GK + x], &b0, &b1);
-            }
-          }
+        };
+        if (large)
+          products(std::true_type{});
+        else
+          products(std::false_type{});
       }
 
       // softmax: the lane holds rows g, g + 8, keys 2t, 2t + 1 of each column tile
@@ -629,34 +680,40 @@ __global__ void __launch_bounds__(PA_THREADS, 2) k_pattn(const AttnArgs A) {
           }
         }
       } else {
-        // words of up to four codes: NT codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
-        constexpr int W = NT < 4 ? NT : 4;
-        uint32_t sc[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const int row = 2 * t + 8 * k, blk = SB > 1 ? g * NT / 32 : 0;
-          sc[k] = scale_pair(scv[row * SB + blk], scv[(row + 1) * SB + blk]);
-        }
-#pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += W) {
-          uint32_t x[4];
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const int row = 2 * t + (k & 1) + (k >> 1) * 8, byte = g * NT + n0;
-            const uint8_t *src = st + Cfg::KV + pa_piece<Cfg>(row, byte / 16) * 16 + byte % 16;
-            x[k] = W == 4 ? *reinterpret_cast<const uint32_t *>(src)
-                          : (uint32_t) * reinterpret_cast<const uint16_t *>(src);
+        auto products = [&](auto two) {
+          // words of up to four codes: NT codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
+          constexpr int W = NT < 4 ? NT : 4;
+          uint32_t sc[2];
+  #pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const int row = 2 * t + 8 * k, blk = SB > 1 ? g * NT / 32 : 0;
+            sc[k] = scale_pair(scv[row * SB + blk] + (decltype(two)::value ? 0 : 120), scv[(row + 1) * SB + blk] + (decltype(two)::value ? 0 : 120));
           }
-#pragma unroll
-          for (int n = 0; n < W; n++) {
-            const uint32_t sel = n | n << 4 | (4 + n) << 8 | (4 + n) << 12;
-            const uint32_t b0 = e4m3x2_value(__byte_perm(x[0], x[1], sel), sc[0]);
-            const uint32_t b1 = e4m3x2_value(__byte_perm(x[2], x[3], sel), sc[1]);
-#pragma unroll
-            for (int mt = 0; mt < MT; mt++)
-              mma_parts<QP, 1>(o[mt][n0 + n], pf[mt], &b0, &b1);
+  #pragma unroll
+          for (int n0 = 0; n0 < NT; n0 += W) {
+            uint32_t x[4];
+  #pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const int row = 2 * t + (k & 1) + (k >> 1) * 8, byte = g * NT + n0;
+              const uint8_t *src = st + Cfg::KV + pa_piece<Cfg>(row, byte / 16) * 16 + byte % 16;
+              x[k] = W == 4 ? *reinterpret_cast<const uint32_t *>(src)
+                            : (uint32_t) * reinterpret_cast<const uint16_t *>(src);
+            }
+  #pragma unroll
+            for (int n = 0; n < W; n++) {
+              const uint32_t sel = n | n << 4 | (4 + n) << 8 | (4 + n) << 12;
+              const uint32_t b0 = pa_codes<decltype(two)::value>(__byte_perm(x[0], x[1], sel), sc[0]);
+              const uint32_t b1 = pa_codes<decltype(two)::value>(__byte_perm(x[2], x[3], sel), sc[1]);
+  #pragma unroll
+              for (int mt = 0; mt < MT; mt++)
+                mma_parts<QP, 1>(o[mt][n0 + n], pf[mt], &b0, &b1);
+            }
           }
-        }
+        };
+        if (large)
+          products(std::true_type{});
+        else
+          products(std::false_type{});
       }
       __syncwarp();
     }
@@ -750,7 +807,7 @@ __global__ void __launch_bounds__(256) k_pattn_merge(const AttnArgs A) {
     const int tok = it - items[b];
     const float *src =
         A.part + ((size_t)parts[b] + ((size_t)tok * A.heads + head) * S.splits) * (DH + 2);
-    // lane i holds the maximum and sum of range i (at most 16)
+    // lane i holds the maximum and sum of slice i (at most 32)
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < S.splits) ml = *reinterpret_cast<const float2 *>(src + lane * (DH + 2) + DH);
     float M = ml.x;

@@ -175,7 +175,7 @@ __device__ __forceinline__ int pw_piece(int row, int c) { return row * 128 + ((c
 // What every role needs of an item.
 struct PwItem {
   SeqCut S;
-  int b, row0, kvh, split, r0, R;  // R: rows of the item
+  int b, row0, kvh, range, r0, R;  // R: rows of the item
   int k0, k1, nk;                  // first key, end, key tiles
 };
 
@@ -188,18 +188,24 @@ __device__ __forceinline__ bool pw_item(const AttnArgs &A, const int *items, con
   int j = it - items[I.b];
   const int rt = j % tiles;
   j /= tiles;
-  I.split = j % I.S.splits;
-  I.kvh = j / I.S.splits;
+  I.range = j % I.S.ranges;
+  I.kvh = j / I.S.ranges;
   I.r0 = rt * PW_RT;
   I.R = min(PW_RT, rows - I.r0);
   const int pos_lo = I.S.first + I.r0 / A.group, pos_hi = I.S.first + (I.r0 + I.R - 1) / A.group;
-  int k0 = I.S.k_lo + I.split * I.S.keys, k1 = min(I.S.k_hi, k0 + I.S.keys);
+  int k0 = I.S.k_lo + I.range * I.S.keys, k1 = min(I.S.k_hi, k0 + I.S.keys);
   if (A.window > 0) k0 = max(k0, (pos_lo - A.window + 1) & ~(PA_TK - 1));
   k1 = min(k1, pos_hi + 1);
   I.k0 = k0;
   I.k1 = k1;
   I.nk = k1 > k0 ? ceil_div(k1 - k0, PW_TK) : 0;
   return !(I.S.splits > 1 && parts[I.b + 1] > A.part_rows);
+}
+
+// Key tiles i of the item that half t of the CTA takes: from, from + by, ..;
+// none where the half is idle.
+__device__ __forceinline__ bool pw_idle(const PwItem &I, int t) {
+  return I.nk == 0 || (I.S.streams ? t >= I.nk : t * 128 >= I.R);
 }
 
 // Whether rows at positions lo .. hi all see keys key0 .. key0 + 127.
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   if (!A.follows) pdl_wait();
   pdl_trigger();
   scan_seqs<PW_THREADS>(A, items, parts, [&](const SeqCut &s) {
-    return s.m * A.group >= A.wide_from ? A.C.H * s.splits * ceil_div(s.m * A.group, PW_RT) : 0;
+    return s.wide ? A.C.H * s.ranges * ceil_div(s.m * A.group, PW_RT) : 0;
   });
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -278,21 +284,23 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       if (I.nk == 0) continue;
       const int pos_lo = I.S.first + I.r0 / A.group,
                 pos_hi = I.S.first + (I.r0 + I.R - 1) / A.group;
-      if (n_item > 0 && !pw_wait(q_empty, (n_item - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      for (int x = tid; x < PW_RT * (DH / 8); x += PW_LOADERS) {
-        const int r = x / (DH / 8), c = x % (DH / 8);
-        if (I.R <= 128 && r >= 128) break;
-        const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
-        const bf16 *src = static_cast<const bf16 *>(A.q) +
-                          (r < I.R ? (int64_t)(I.row0 + tok) * A.ldq + head * DH + c * 8 : 0);
-        cp_async16(smem_u32(sm + Cfg::Q + (r >> 7) * Cfg::TILE + (c >> 3) * Cfg::HALF +
-                            pw_piece(r & 127, c & 7)),
-                   src, r < I.R ? 16 : 0);
-      }
-      arrive_behind_copies(q_in);
+      // Queries, behind the item's first keys and values: those need no more than
+      // their stages, the queries' place is in use until the last item is done.
+      auto load_queries = [&]() {
+        if (n_item > 0 && !pw_wait(q_empty, (n_item - 1) & 1)) return false;
+        for (int x = tid; x < PW_RT * (DH / 8); x += PW_LOADERS) {
+          const int r = x / (DH / 8), c = x % (DH / 8);
+          if (I.R <= 128 && r >= 128) break;
+          const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
+          const bf16 *src = static_cast<const bf16 *>(A.q) +
+                            (r < I.R ? (int64_t)(I.row0 + tok) * A.ldq + head * DH + c * 8 : 0);
+          cp_async16(smem_u32(sm + Cfg::Q + (r >> 7) * Cfg::TILE + (c >> 3) * Cfg::HALF +
+                              pw_piece(r & 127, c & 7)),
+                     src, r < I.R ? 16 : 0);
+        }
+        arrive_behind_copies(q_in);
+        return true;
+      };
 
       // pages of a key tile: lane j < 8 holds the row of the cache's key plane
       // where keys 16 j .. 16 j + 15 begin (rows of 64 bytes and more: 32 bits
@@ -390,6 +398,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
             if (tid == 0) tc_mbar_arrive(v_in + st);
           }
           cells = next;
+          if (i == 0 && ok) ok = load_queries();
         }
       } else {
         // codes through registers: the next unit's are fetched before this
@@ -470,6 +479,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
             else if (i + 1 < I.nk)
               fetch(i + 1, 0);
           }
+          if (i == 0 && ok) ok = load_queries();
         }
       }
       n_item++;
@@ -487,68 +497,75 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       constexpr uint32_t idS = idesc_bf16_f32(128, PW_TK);
       constexpr uint32_t idO = idesc_bf16_f32(128, DH) | (1u << 16);  // V: MN-major
       const int t = warp - 12;
-      const uint64_t q0 = smem_desc_sw128(sm + Cfg::Q + t * Cfg::TILE);
-      const uint64_t k0 = smem_desc_sw128(sm + Cfg::K);
+      const uint64_t q0 = smem_desc_sw128(sm + Cfg::Q), k0 = smem_desc_sw128(sm + Cfg::K);
       const uint64_t v0 = pw_desc_v(smem_u32(sm + Cfg::V), Cfg::HALF);
       const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * DH;
       uint32_t n_item = 0, n_tile = 0, n_t = 0;
       bool ok = true;
-      auto scores = [&](int i) {
-        const uint64_t kd = k0 + (uint64_t)(((n_tile + i) % ST) * (Cfg::TILE >> 4));
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < DH / 16; k++) {
-            const uint64_t at = (uint64_t)((k >> 2) * (Cfg::HALF >> 4) + 2 * (k & 3));
-            umma_bf16(tS, q0 + at, kd + at, idS, k > 0 ? 1u : 0u);
-          }
-          umma_commit(s_full + t);
-        }
-        __syncwarp();
-      };
       for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
         PwItem I;
         if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
-        // Every item's queries are waited for, an idle tile's too, and the second
-        // arrival on q_empty comes from here where the tile is idle: a warp
-        // that the phases overtook would take an old phase for the next.
+        // Every item's queries are waited for, by an idle half too, and its
+        // arrival on q_empty comes from here: a warp that the phases overtook
+        // would take an old phase for the next.
         ok = pw_wait(q_full, n_item & 1);
         if (!ok) break;
-        if (t == 1 && I.R <= 128) {
+        if (pw_idle(I, t)) {
           if (lane == 0) tc_mbar_arrive(q_empty);
         } else {
-          ok = pw_wait(k_full + n_tile % ST, n_tile / ST & 1);
+          // streams: both halves have the queries of the first tile
+          const uint64_t qd = q0 + (I.S.streams ? 0 : (uint64_t)(t * (Cfg::TILE >> 4)));
+          const int from = I.S.streams ? t : 0, by = I.S.streams ? 2 : 1;
+          auto scores = [&](int i) {
+            const uint64_t kd = k0 + (uint64_t)(((n_tile + i) % ST) * (Cfg::TILE >> 4));
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < DH / 16; k++) {
+                const uint64_t at = (uint64_t)((k >> 2) * (Cfg::HALF >> 4) + 2 * (k & 3));
+                umma_bf16(tS, qd + at, kd + at, idS, k > 0 ? 1u : 0u);
+              }
+              umma_commit(s_full + t);
+            }
+            __syncwarp();
+          };
+          ok = pw_wait(k_full + (n_tile + from) % ST, (n_tile + from) / ST & 1);
           if (!ok) break;
           tc_fence_after();
-          scores(0);
-          for (int i = 0; i < I.nk; i++) {
-            // PV of tile i in two parts as P comes, then the scores of tile i + 1.
-            // The softmax has waited for V before it hands P on.
-            const uint64_t vd = v0 + (uint64_t)(((n_tile + i) % ST) * (Cfg::TILE >> 4));
-            const bool more = i + 1 < I.nk;
-            if (more) ok = pw_wait(k_full + (n_tile + i + 1) % ST, (n_tile + i + 1) / ST & 1);
-            ok = ok && pw_wait(p_full + 2 * t, (n_t + i) & 1);
+          scores(from);
+          for (int i = from; i < I.nk; i += by) {
+            // PV of tile i in two parts as P comes, then the scores of the next
+            // tile. The softmax has waited for V before it hands P on.
+            const int st = (n_tile + i) % ST;
+            const uint64_t vd = v0 + (uint64_t)(st * (Cfg::TILE >> 4));
+            const int next = i + by;
+            const bool more = next < I.nk;
+            if (more) ok = pw_wait(k_full + (n_tile + next) % ST, (n_tile + next) / ST & 1);
+            ok = ok && pw_wait(p_full + 2 * t, n_t & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 6; k++)
                 umma_ts(tO, tS + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO,
-                        (i > 0 || k > 0) ? 1u : 0u);
+                        (i > from || k > 0) ? 1u : 0u);
             }
             __syncwarp();
-            ok = pw_wait(p_full + 2 * t + 1, (n_t + i) & 1);
+            ok = pw_wait(p_full + 2 * t + 1, n_t & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int k = 6; k < 8; k++)
                 umma_ts(tO, tS + k * 8, vd + (uint64_t)(k * (2048 >> 4)), idO, 1u);
+              umma_commit(v_empty + st);
+              if (by == 2 || I.R <= 128) umma_commit(v_empty + st);  // of the other half
               if (!more) umma_commit(o_full + t);
             }
             __syncwarp();
-            if (more) scores(i + 1);
+            n_t++;
+            if (more) scores(next);
           }
-          n_t += I.nk;
+          if (!ok) break;
         }
         n_item++;
         n_tile += I.nk;
@@ -569,11 +586,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
         PwItem I;
         if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
-        pass_on(q_in, q_full, n_item & 1);
         for (int i = 0; ok && i < I.nk; i++) {
           const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
           pass_on(k_in + st, k_full + st, use & 1);
           pass_on(v_in + st, v_full + st, use & 1);
+          if (i == 0) pass_on(q_in, q_full, n_item & 1);
         }
         n_item++;
         n_tile += I.nk;
@@ -592,36 +609,36 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
       PwItem I;
       if (!pw_item(A, items, parts, it, I)) continue;
-      // Products complete in the order of their issue: once the scores of tile i
-      // are there, K of tile i, V and P of tile i - 1 have been read. One thread
-      // of each row tile gives stages back (of the only one twice).
-      auto give_back = [&](uint64_t *empty) {
-        if (row == 0) {
-          tc_mbar_arrive(empty);
-          if (I.R <= 128) tc_mbar_arrive(empty);
-        }
-      };
-      const int r = t * 128 + row;  // row of the item
+      // row of the item, and the half's key tiles: i = from, from + by, ..
+      const int r = (I.S.streams ? 0 : t * 128) + row;
+      const int from = I.S.streams ? t : 0, by = I.S.streams ? 2 : 1;
+      const bool idle = pw_idle(I, t);
       const int tok = (I.r0 + r) / A.group, head = I.kvh * A.group + (I.r0 + r) % A.group;
       const int pos = r < I.R ? I.S.first + tok : -1;
-      const int pos_lo = I.S.first + (I.r0 + t * 128) / A.group;
-      const int pos_hi = I.S.first + (I.r0 + min(I.R, t * 128 + 128) - 1) / A.group;
-      if (t * 128 >= I.R) {  // no second tile: the whole warpgroup skips
+      const int top = I.r0 + (I.S.streams ? 0 : t * 128);
+      const int pos_lo = I.S.first + top / A.group;
+      const int pos_hi = I.S.first + (min(I.r0 + I.R, top + 128) - 1) / A.group;
+      if (idle && !I.S.streams && I.nk > 0) {  // no rows: the whole warpgroup skips
         n_tile += I.nk;
         continue;
       }
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < I.nk; i++) {
+      for (int i = from; !idle && i < I.nk; i += by) {
         const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
         const int key0 = I.k0 + i * PW_TK;
         // (in this order: V's phase is known to be this tile's once the scores are)
-        if (!pw_wait(s_full + t, (n_t + i) & 1) || !pw_wait(v_full + st, use & 1)) {
+        if (!pw_wait(s_full + t, n_t & 1) || !pw_wait(v_full + st, use & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        give_back(k_empty + st);
-        if (i > 0) give_back(v_empty + (n_tile + i - 1) % ST);
+        n_t++;
+        // The scores are there, so K has been read: one thread gives its stage
+        // back, for the other half too where that does not take the tile.
+        if (row == 0) {
+          tc_mbar_arrive(k_empty + st);
+          if (by == 2 || I.R <= 128) tc_mbar_arrive(k_empty + st);
+        }
         const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
         const bool all = pw_all_see(A, I, key0, pos_lo, pos_hi) &&
                          !(fl[0] | fl[1] | fl[2] | fl[3]);
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         mx *= A.scale_log2;
         // O keeps its reference until the maximum has outgrown it by 2^8
         const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
-        if (i > 0 && __any_sync(FULL_MASK, grow)) {
+        if (i > from && __any_sync(FULL_MASK, grow)) {
           const float corr = grow ? pa_exp2(m - mx) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < DH / 16; c++) {
@@ -704,27 +721,25 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         l += sum.x + sum.y;
       }
       if (!ok) break;
-      if (I.nk > 0) {
+      if (!idle) {
         if (!pw_wait(o_full + t, n_item & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        give_back(v_empty + (n_tile + I.nk - 1) % ST);
         if (row == 0) tc_mbar_arrive(q_empty);
         n_item++;
       }
       n_tile += I.nk;
-      n_t += I.nk;
       const bool on = r < I.R;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float *part = A.part + ((size_t)parts[I.b] + ((size_t)tok * A.heads + head) * I.S.splits +
-                              I.split) * (DH + 2);
+                              (I.S.streams ? 2 * I.range + t : I.range)) * (DH + 2);
       bf16 *dst = static_cast<bf16 *>(A.out) + (int64_t)(I.row0 + tok) * A.ldo + head * DH;
 #pragma unroll
       for (int c = 0; c < DH / 32; c++) {
         uint32_t s[32];
-        if (I.nk > 0) {
+        if (!idle) {
           pw_ld32(tO + 32 * c, s);
           pw_wait_ld();
         } else {
