@@ -41,7 +41,7 @@ constexpr int PA_UNIT_ROWS = 32;     // rows of a unit in the split rule
 constexpr int PA_SPLIT_UNITS = 256;  // units x splits aimed at per sequence
 constexpr int PA_MAX_SPLITS = 16;
 constexpr int PA_MIN_KEYS = 256;     // least keys of a split ..
-constexpr int PA_ROW_KEYS = 32;      // .. and for each row of a unit
+constexpr int PA_ROW_BYTES = 64;     // .. and bytes of a key's entry for each row of a unit
 // The same of sequences that go to the tcgen05 kernel: tiles of 256 rows, one
 // CTA per SM, splits long enough that writing O in fp32 stays below a tenth.
 // Of sequences of at most PA_STREAM_ROWS rows both halves of a CTA take the same
@@ -65,7 +65,7 @@ struct SeqCut {
 __device__ __host__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_heads, int window,
-                                          bool wide_kernel) {
+                                          bool wide_kernel, int es) {
   SeqCut s;
   s.m = m;
   s.first = len - m;
@@ -85,7 +85,7 @@ __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_head
     const int units = max(1, kv_heads * ceil_div(rows, PA_UNIT_ROWS));
     // (writing and joining a slice stays below a tenth of reading its keys)
     n = min(ceil_div(PA_SPLIT_UNITS, units),
-            ceil_div(span, max(PA_MIN_KEYS, PA_ROW_KEYS * min(rows, PA_UNIT_ROWS))));
+            ceil_div(span, max(PA_MIN_KEYS, PA_ROW_BYTES / es * min(rows, PA_UNIT_ROWS))));
   }
   n = max(1, min(n, PA_MAX_SPLITS));
   s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);
@@ -107,6 +107,7 @@ struct AttnArgs {
   float *part;       // [part_rows][DH + 2]: O (not divided), maximum (base 2), sum
   int part_rows;
   int wide;          // whether k_pattn_wide takes part (its types and head sizes)
+  int es;            // bytes of a cache element
   int follows;       // k_pattn_wide: k_pattn of the same call runs before it
 };
 
@@ -120,12 +121,12 @@ __device__ __forceinline__ SeqCut cut_of(const AttnArgs &A, int b, int &row0, in
     const int len = A.R.len[b];
     if (hi - lo <= A.max_rows && len >= 0 && len <= A.max_len) {
       row0 = lo;
-      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, A.wide);
+      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, A.wide, A.es);
     }
     flag_rows(A.R, RLT_PAGED_BAD_ROWS);
   }
   row0 = 0;
-  return cut_seq(0, 0, A.group, A.C.H, A.window, false);
+  return cut_seq(0, 0, A.group, A.C.H, A.window, false, A.es);
 }
 
 // Running sums over the sequences, in shared memory: items[b] items and
