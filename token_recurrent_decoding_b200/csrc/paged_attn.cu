@@ -119,7 +119,7 @@ template <typename T>
 cudaError_t launch_merge(const AttnArgs &A, int dh, int sms, cudaStream_t st) {
   const int64_t warps = (int64_t)A.R.rows * A.heads;
   const int grid = (int)(warps / 8 + 1 < 4 * sms ? warps / 8 + 1 : 4 * sms);
-  const size_t smem = 2 * (A.R.n + 1) * sizeof(int);
+  const size_t smem = Plan::bytes(A.R.n);
   switch (dh) {
     case 16: return launch_pdl(k_pattn_merge<T, 16>, grid, 256, smem, st, A);
     case 32: return launch_pdl(k_pattn_merge<T, 32>, grid, 256, smem, st, A);

@@ -40,8 +40,10 @@ constexpr int PA_TK = 16;            // keys of a tile
 constexpr int PA_UNIT_ROWS = 32;     // rows of a unit in the split rule
 constexpr int PA_SPLIT_UNITS = 256;  // units x splits aimed at per sequence
 constexpr int PA_MAX_SPLITS = 16;
-constexpr int PA_MIN_KEYS = 256;     // least keys of a split ..
-constexpr int PA_ROW_BYTES = 64;     // .. and bytes of a key's entry for each row of a unit
+constexpr int PA_SHORT_SPLITS = 4;   // splits of ..
+constexpr int PA_MIN_KEYS = 256;     // .. at least so many keys, and more of ..
+constexpr int PA_LONG_KEYS = 2048;   // .. at least these
+constexpr int PA_ROW_BYTES = 64;     // keys x element bytes of a split for each row of a unit
 // The same of sequences that go to the tcgen05 kernel: tiles of 256 rows, one
 // CTA per SM, splits long enough that writing O in fp32 stays below a tenth.
 // Of sequences of at most PA_STREAM_ROWS rows both halves of a CTA take the same
@@ -83,9 +85,14 @@ __device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_head
     n = min(PA_WIDE_UNITS / (kv_heads * ceil_div(rows, PA_WIDE_ROWS)), ceil_div(span, PA_WIDE_KEYS));
   } else {
     const int units = max(1, kv_heads * ceil_div(rows, PA_UNIT_ROWS));
-    // (writing and joining a slice stays below a tenth of reading its keys)
-    n = min(ceil_div(PA_SPLIT_UNITS, units),
-            ceil_div(span, max(PA_MIN_KEYS, PA_ROW_BYTES / es * min(rows, PA_UNIT_ROWS))));
+    // Up to four ranges of 256 keys and more for the latency of few sequences;
+    // beyond that a range's own start and end (about 2 us) wants 2048 keys to
+    // pay: 32 steps in 8 bits of 2000-4096 positions took 169, 145, 135, 155 us
+    // with ranges of at least 256, 512, 1024, 2048. Writing and joining a slice
+    // stays below a tenth of reading its keys.
+    n = max(min(PA_SHORT_SPLITS, ceil_div(span, PA_MIN_KEYS)), ceil_div(span, PA_LONG_KEYS));
+    n = min(min(n, ceil_div(PA_SPLIT_UNITS, units)),
+            ceil_div(span, PA_ROW_BYTES / es * min(rows, PA_UNIT_ROWS)));
   }
   n = max(1, min(n, PA_MAX_SPLITS));
   s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);
@@ -111,36 +118,41 @@ struct AttnArgs {
   int follows;       // k_pattn_wide: k_pattn of the same call runs before it
 };
 
-// Rows and cut of sequence b; rows 0 where it takes no part in the call, `fine`
-// cleared where its rows are none of the call.
-__device__ __forceinline__ SeqCut cut_of(const AttnArgs &A, int b, int &row0, int &fine) {
-  int lo, hi;
-  if (!seq_rows(A.R, b, lo, hi)) {
-    fine = 0;
-  } else {
-    const int len = A.R.len[b];
-    if (hi - lo <= A.max_rows && len >= 0 && len <= A.max_len) {
-      row0 = lo;
-      return cut_seq(hi - lo, len, A.group, A.C.H, A.window, A.wide, A.es);
-    }
-    flag_rows(A.R, RLT_PAGED_BAD_ROWS);
+// What a block keeps of the call's sequences, in shared memory: 4 (n + 1) ints.
+struct Plan {
+  int *items, *parts;  // items and partial rows before sequence b
+  int *cu, *len;       // as given; len -1 where the sequence takes no part
+  __device__ Plan(int *at, int n)
+      : items(at), parts(at + n + 1), cu(at + 2 * (n + 1)), len(at + 3 * (n + 1)) {}
+  static __host__ __device__ int bytes(int n) { return 4 * (n + 1) * (int)sizeof(int); }
+  __device__ SeqCut cut(const AttnArgs &A, int b) const {
+    const int l = len[b], m = l < 0 ? 0 : cu[b + 1] - cu[b];
+    return cut_seq(m, max(l, 0), A.group, A.C.H, A.window, A.wide, A.es);
   }
-  row0 = 0;
-  return cut_seq(0, 0, A.group, A.C.H, A.window, false, A.es);
-}
+};
 
-// Running sums over the sequences, in shared memory: items[b] items and
-// parts[b] partial rows come before sequence b. Every thread of the block calls it.
+// Fills the plan. Every thread of the block calls it.
 template <int THREADS, class Items>
-__device__ void scan_seqs(const AttnArgs &A, int *items, int *parts, Items count) {
+__device__ void make_plan(const AttnArgs &A, const Plan &P, Items count) {
   __shared__ int s_i[THREADS / 32], s_p[THREADS / 32];
   const int per = ceil_div(A.R.n, THREADS), b0 = threadIdx.x * per, b1 = min(A.R.n, b0 + per);
   int ni = 0, np = 0, fine = 1;
   for (int b = b0; b < b1; b++) {
-    int row0;
-    const SeqCut s = cut_of(A, b, row0, fine);
-    items[b] = ni;  // within this thread's sequences, completed below
-    parts[b] = np;
+    int lo, hi, len = A.R.len[b];
+    if (!seq_rows(A.R, b, lo, hi)) {
+      fine = 0;
+      len = -1;
+    } else if (hi - lo > A.max_rows || len < 0 || len > A.max_len) {
+      flag_rows(A.R, RLT_PAGED_BAD_ROWS);
+      len = -1;
+    }
+    P.cu[b] = lo;
+    P.cu[b + 1] = hi;  // the same number the owner of sequence b + 1 writes
+    P.len[b] = len;
+    const SeqCut s =
+        cut_seq(len < 0 ? 0 : hi - lo, max(len, 0), A.group, A.C.H, A.window, A.wide, A.es);
+    P.items[b] = ni;  // within this thread's sequences, completed below
+    P.parts[b] = np;
     ni += s.m > 0 ? count(s) : 0;
     np += s.splits > 1 ? s.m * A.heads * s.splits : 0;
   }
@@ -172,12 +184,12 @@ __device__ void scan_seqs(const AttnArgs &A, int *items, int *parts, Items count
   }
   const int oi = wi + ii - ni, op = wp + pp - np;
   for (int b = b0; b < b1; b++) {
-    items[b] += oi;
-    parts[b] += op;
+    P.items[b] += oi;
+    P.parts[b] += op;
   }
   if (threadIdx.x == 0) {
-    items[A.R.n] = fine ? ti : 0;
-    parts[A.R.n] = tp;
+    P.items[A.R.n] = fine ? ti : 0;
+    P.parts[A.R.n] = tp;
   }
   __syncthreads();
 }
@@ -211,13 +223,13 @@ template <int KIND, int DH, int MT> struct PaCfg {
   static constexpr int STAGE = 2 * KV + (E4 ? 2 * PA_TK * SB : 0);
   // CTAs of an SM the registers are cut for, and stages that fit as often
   static constexpr int CTAS = MT == 1 && QP == 1 ? 3 : 2;
-  static constexpr int STAGES = DH == 128 && (KIND == PA_F32 || (KIND == PA_BF16 && MT == 1)) ? 2 : 3;
+  static constexpr int STAGES = KIND == PA_E4M3 || (DH == 128 && (KIND == PA_F32 || MT == 1)) ? 2 : 3;
   static constexpr int RT = 16 * MT;
   static constexpr int RING = 4 * STAGES * STAGE;
   static constexpr int JOIN = 4 * RT * DH * 4;  // O of the four warps, over the ring
   static constexpr int MAIN = RING > JOIN ? RING : JOIN;
   static constexpr int ML = 2 * 4 * RT * 4;     // maxima and sums of the four warps
-  static int bytes(int n) { return MAIN + ML + 2 * (n + 1) * 4; }
+  static int bytes(int n) { return MAIN + ML + Plan::bytes(n); }
 };
 
 // Place of 16-byte piece c of row r in a tile, chosen so that the lanes that
@@ -285,17 +297,28 @@ template <int P> __device__ __forceinline__ void split_pair(float a, float b, ui
 }
 
 // c += sum of the products of parts i of a and j of b with i + j < max(QP, KP).
+// Products of parts are summed from zero, smallest first, and added to c with
+// one rounding: the tensor cores cut what they add to, and dozens of cuts of a
+// long sum cost more than fp32's own additions (1.3e-6 of the result against
+// 7e-7 over 1024 keys).
 template <int QP, int KP>
 __device__ __forceinline__ void mma_parts(float c[4], const uint32_t a[][4], const uint32_t *b0,
                                           const uint32_t *b1) {
   constexpr int N = QP > KP ? QP : KP;
+  if constexpr (N == 1) {
+    mma16816(c, a[0], b0[0], b1[0]);
+  } else {
+    float sum[4] = {};
 #pragma unroll
-  for (int s = N - 1; s >= 0; s--)  // smallest products first
+    for (int s = N - 1; s >= 0; s--)
 #pragma unroll
-    for (int j = 0; j < KP; j++) {
-      const int i = s - j;
-      if (i >= 0 && i < QP) mma16816(c, a[i], b0[j], b1[j]);
-    }
+      for (int j = 0; j < KP; j++) {
+        const int i = s - j;
+        if (i >= 0 && i < QP) mma16816(sum, a[i], b0[j], b1[j]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; e++) c[e] += sum[e];
+  }
 }
 
 // Two codes as bf16 values: scale2 is their scales, or with TWO unset 2^120 of them.
@@ -325,28 +348,27 @@ __global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn
   constexpr int RT = Cfg::RT, KS = DH / 16, NT = DH / 8;
   extern __shared__ __align__(128) uint8_t pa_sm[];
   float *s_m = reinterpret_cast<float *>(pa_sm + Cfg::MAIN), *s_l = s_m + 4 * RT;
-  int *items = reinterpret_cast<int *>(s_l + 4 * RT), *parts = items + A.R.n + 1;
+  const Plan P(reinterpret_cast<int *>(s_l + 4 * RT), A.R.n);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t *ring = pa_sm + warp * Cfg::STAGES * Cfg::STAGE;
   const uint32_t ring_u = smem_u32(ring);
 
   pdl_wait();
   pdl_trigger();
-  scan_seqs<PA_THREADS>(A, items, parts, [&](const SeqCut &s) {
+  make_plan<PA_THREADS>(A, P, [&](const SeqCut &s) {
     return s.wide ? 0 : A.C.H * s.splits * ceil_div(s.m * A.group, RT);
   });
-  const int total = items[A.R.n];
+  const int total = P.items[A.R.n];
 
   for (int it = blockIdx.x; it < total; it += gridDim.x) {
-    const int b = find_seq(items, A.R.n, it);
-    int row0, fine;
-    const SeqCut S = cut_of(A, b, row0, fine);
+    const int b = find_seq(P.items, A.R.n, it), row0 = P.cu[b];
+    const SeqCut S = P.cut(A, b);
     const int tiles = ceil_div(S.m * A.group, RT);
-    int j = it - items[b];
+    int j = it - P.items[b];
     const int rt = j % tiles;
     j /= tiles;
     const int split = j % S.splits, kvh = j / S.splits;
-    if (S.splits > 1 && parts[b + 1] > A.part_rows) {
+    if (S.splits > 1 && P.parts[b + 1] > A.part_rows) {
       if (threadIdx.x == 0) flag_rows(A.R, RLT_PAGED_BAD_ROWS);
       continue;
     }
@@ -359,31 +381,6 @@ __global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn
     const int t0 = k0 / PA_TK, t1 = k1 > k0 ? ceil_div(k1, PA_TK) : t0;
     const int my = t1 - t0 > warp ? (t1 - t0 - warp + 3) / 4 : 0;  // this warp's tiles
 
-    // queries, in product order; rows behind the last are zeros
-    uint32_t qf[MT][KS][QP][4];
-    int pos[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-      for (int hrow = 0; hrow < 2; hrow++) {
-        const int r = mt * 16 + hrow * 8 + g;
-        const bool on = r < R;
-        const int tok = (r0 + r) / A.group, head = kvh * A.group + (r0 + r) % A.group;
-        pos[mt][hrow] = on ? S.first + tok : -1;
-        const TQ *src =
-            static_cast<const TQ *>(A.q) + (int64_t)(row0 + tok) * A.ldq + head * DH;
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-          for (int half = 0; half < 2; half++) {
-            const float x = on ? to_f(src[head_order<KIND, DH>(ks, t, 2 * half)]) : 0.f;
-            const float y = on ? to_f(src[head_order<KIND, DH>(ks, t, 2 * half + 1)]) : 0.f;
-            uint32_t p[QP];
-            split_pair<QP>(x, y, p);
-#pragma unroll
-            for (int i = 0; i < QP; i++) qf[mt][ks][i][2 * half + hrow] = p[i];
-          }
-      }
     float o[MT][NT][4], m[MT][2], l[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
@@ -452,6 +449,31 @@ __global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn
       if (i < my) load(i);
       cp_async_commit();
     }
+    // queries, in product order; rows behind the last are zeros
+    uint32_t qf[MT][KS][QP][4];
+    int pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int hrow = 0; hrow < 2; hrow++) {
+        const int r = mt * 16 + hrow * 8 + g;
+        const bool on = r < R;
+        const int tok = (r0 + r) / A.group, head = kvh * A.group + (r0 + r) % A.group;
+        pos[mt][hrow] = on ? S.first + tok : -1;
+        const TQ *src =
+            static_cast<const TQ *>(A.q) + (int64_t)(row0 + tok) * A.ldq + head * DH;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const float x = on ? to_f(src[head_order<KIND, DH>(ks, t, 2 * half)]) : 0.f;
+            const float y = on ? to_f(src[head_order<KIND, DH>(ks, t, 2 * half + 1)]) : 0.f;
+            uint32_t p[QP];
+            split_pair<QP>(x, y, p);
+#pragma unroll
+            for (int i = 0; i < QP; i++) qf[mt][ks][i][2 * half + hrow] = p[i];
+          }
+      }
     for (int i = 0; i < my; i++) {
       cp_async_wait<Cfg::STAGES - 2>();
       __syncwarp();
@@ -765,7 +787,7 @@ __global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn
       }
       const int tok = (r0 + r) / A.group, head = kvh * A.group + (r0 + r) % A.group;
       if (S.splits > 1) {
-        const size_t p = (size_t)parts[b] + ((size_t)tok * A.heads + head) * S.splits + split;
+        const size_t p = (size_t)P.parts[b] + ((size_t)tok * A.heads + head) * S.splits + split;
         float *dst = A.part + p * (DH + 2);
 #pragma unroll
         for (int e = 0; e < 4; e += 2)
@@ -795,19 +817,20 @@ __global__ void __launch_bounds__(PA_THREADS, PaCfg<KIND, DH, MT>::CTAS) k_pattn
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) k_pattn_merge(const AttnArgs A) {
   extern __shared__ int pm_sm[];
-  int *items = pm_sm, *parts = pm_sm + A.R.n + 1;
+  const Plan P(pm_sm, A.R.n);
+  // (the caller's inputs are complete: the kernel before waited for them)
+  make_plan<256>(A, P, [&](const SeqCut &s) { return s.splits > 1 ? s.m : 0; });
   pdl_wait();
-  scan_seqs<256>(A, items, parts, [&](const SeqCut &s) { return s.splits > 1 ? s.m : 0; });
-  const int total = items[A.R.n] * A.heads;
+  const int total = P.items[A.R.n] * A.heads;
   const int lane = threadIdx.x & 31;
   for (int x = blockIdx.x * 8 + (threadIdx.x >> 5); x < total; x += gridDim.x * 8) {
-    const int head = x % A.heads, it = x / A.heads, b = find_seq(items, A.R.n, it);
-    if (parts[b + 1] > A.part_rows) continue;
-    int row0, fine;
-    const SeqCut S = cut_of(A, b, row0, fine);
-    const int tok = it - items[b];
+    const int head = x % A.heads, it = x / A.heads, b = find_seq(P.items, A.R.n, it);
+    if (P.parts[b + 1] > A.part_rows) continue;
+    const int row0 = P.cu[b];
+    const SeqCut S = P.cut(A, b);
+    const int tok = it - P.items[b];
     const float *src =
-        A.part + ((size_t)parts[b] + ((size_t)tok * A.heads + head) * S.splits) * (DH + 2);
+        A.part + ((size_t)P.parts[b] + ((size_t)tok * A.heads + head) * S.splits) * (DH + 2);
     // lane i holds the maximum and sum of slice i (at most 32)
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < S.splits) ml = *reinterpret_cast<const float2 *>(src + lane * (DH + 2) + DH);

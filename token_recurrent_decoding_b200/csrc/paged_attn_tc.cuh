@@ -57,7 +57,7 @@ template <int DH> struct PwCfg {
   static constexpr int FLAGS = BARS + NBARS * 8;   // [INFO][8] words: unseen keys, strange keys
   static constexpr int SLOT = FLAGS + INFO * 8 * 4;
   static constexpr int PLAN = SLOT + 16;
-  static int bytes(int n) { return PLAN + 2 * (n + 1) * 4 + 1024; }
+  static int bytes(int n) { return PLAN + Plan::bytes(n) + 1024; }
 };
 
 // Warp-uniform bounded wait: the warp leaves together (what follows is often
@@ -179,13 +179,12 @@ struct PwItem {
   int k0, k1, nk;                  // first key, end, key tiles
 };
 
-__device__ __forceinline__ bool pw_item(const AttnArgs &A, const int *items, const int *parts,
-                                        int it, PwItem &I) {
-  I.b = find_seq(items, A.R.n, it);
-  int fine;
-  I.S = cut_of(A, I.b, I.row0, fine);
+__device__ __forceinline__ bool pw_item(const AttnArgs &A, const Plan &P, int it, PwItem &I) {
+  I.b = find_seq(P.items, A.R.n, it);
+  I.row0 = P.cu[I.b];
+  I.S = P.cut(A, I.b);
   const int rows = I.S.m * A.group, tiles = ceil_div(rows, PW_RT);
-  int j = it - items[I.b];
+  int j = it - P.items[I.b];
   const int rt = j % tiles;
   j /= tiles;
   I.range = j % I.S.ranges;
@@ -199,7 +198,7 @@ __device__ __forceinline__ bool pw_item(const AttnArgs &A, const int *items, con
   I.k0 = k0;
   I.k1 = k1;
   I.nk = k1 > k0 ? ceil_div(k1 - k0, PW_TK) : 0;
-  return !(I.S.splits > 1 && parts[I.b + 1] > A.part_rows);
+  return !(I.S.splits > 1 && P.parts[I.b + 1] > A.part_rows);
 }
 
 // Key tiles i of the item that half t of the CTA takes: from, from + by, ..;
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
            *o_full = p_full + 4;  // p_full[t][part of the keys]
   uint32_t *flags = reinterpret_cast<uint32_t *>(sm + Cfg::FLAGS);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Cfg::SLOT);
-  int *items = reinterpret_cast<int *>(sm + Cfg::PLAN), *parts = items + A.R.n + 1;
+  const Plan P(reinterpret_cast<int *>(sm + Cfg::PLAN), A.R.n);
   __shared__ int s_fail;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -261,12 +260,12 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   // let this kernel start) and its own are waited for at the end
   if (!A.follows) pdl_wait();
   pdl_trigger();
-  scan_seqs<PW_THREADS>(A, items, parts, [&](const SeqCut &s) {
+  make_plan<PW_THREADS>(A, P, [&](const SeqCut &s) {
     return s.wide ? A.C.H * s.ranges * ceil_div(s.m * A.group, PW_RT) : 0;
   });
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = items[A.R.n];
+  const int total = P.items[A.R.n];
   volatile int *fail = &s_fail;
 
   if (warp >= 8 && warp < 12) {
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     bool ok = true;
     for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
       PwItem I;
-      if (!pw_item(A, items, parts, it, I)) {
+      if (!pw_item(A, P, it, I)) {
         if (tid == 0) flag_rows(A.R, RLT_PAGED_BAD_ROWS);
         continue;
       }
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       bool ok = true;
       for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
         PwItem I;
-        if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
+        if (!pw_item(A, P, it, I) || I.nk == 0) continue;
         // Every item's queries are waited for, by an idle half too, and its
         // arrival on q_empty comes from here: a warp that the phases overtook
         // would take an old phase for the next.
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       };
       for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
         PwItem I;
-        if (!pw_item(A, items, parts, it, I) || I.nk == 0) continue;
+        if (!pw_item(A, P, it, I) || I.nk == 0) continue;
         for (int i = 0; ok && i < I.nk; i++) {
           const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
           pass_on(k_in + st, k_full + st, use & 1);
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     bool ok = true;
     for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
       PwItem I;
-      if (!pw_item(A, items, parts, it, I)) continue;
+      if (!pw_item(A, P, it, I)) continue;
       // row of the item, and the half's key tiles: i = from, from + by, ..
       const int r = (I.S.streams ? 0 : t * 128) + row;
       const int from = I.S.streams ? t : 0, by = I.S.streams ? 2 : 1;
@@ -746,7 +745,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       n_tile += I.nk;
       const bool on = r < I.R;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float *part = A.part + ((size_t)parts[I.b] + ((size_t)tok * A.heads + head) * I.S.splits +
+      float *part = A.part + ((size_t)P.parts[I.b] + ((size_t)tok * A.heads + head) * I.S.splits +
                               (I.S.streams ? 2 * I.range + t : I.range)) * (DH + 2);
       bf16 *dst = static_cast<bf16 *>(A.out) + (int64_t)(I.row0 + tok) * A.ldo + head * DH;
 #pragma unroll
