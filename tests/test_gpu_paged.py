@@ -390,3 +390,66 @@ def test_tensors_that_do_not_fit_are_refused():
                  (pages.to(E4), torch.zeros((2, 2, 2, 16, 1), dtype=torch.uint8, device="cuda"))):
         with pytest.raises(rlt.RLTError):
             rlt.PagedKV(*args)
+
+
+@pytest.mark.parametrize("kind,m", [("bf16", 2), ("bf16", 50), ("bf16e4", 50), ("f32", 2)])
+def test_pages_behind_four_gigabytes(kind, m):
+    """The sequence's pages are the last of a pool of more than 2^32 bytes (and elements, in 8 bits)."""
+    e4, dtype, page, dh = kind.endswith("e4"), F32 if kind == "f32" else BF16, 1024, 128
+    es = 1 if e4 else 4 if dtype == F32 else 2
+    per_page = 2 * page * dh * es
+    n_pages = 2 ** 32 // per_page + 64
+    cache = rlt.PagedKV.empty(n_pages, page, 1, dh, dtype, rlt.KV_E4M3 if e4 else rlt.KV_PLAIN)
+    L = 1500
+    g = torch.Generator().manual_seed(1)
+    kv = torch.randn((L, 1, 2, dh), generator=g).to(dtype)
+    table = torch.tensor([[n_pages - 1, n_pages - 3]], dtype=torch.int32).cuda()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    d = kv.cuda()
+    rlt.paged_append(cache, table, d[:, :, 0], d[:, :, 1], i32(0, L), i32(L))
+    held = torch.from_numpy(quantised(kv.double().numpy())[0]) if e4 else kv.double()
+    ko, vo = (torch.empty((L, 1, dh), dtype=dtype, device="cuda") for _ in range(2))
+    rlt.paged_read(cache, table, i32(0, L), i32(L), ko, vo)
+    assert torch.equal(ko.double().cpu(), held[:, :, 0])
+    assert torch.equal(vo.double().cpu(), held[:, :, 1])
+    q = torch.randn((m, 1, dh), generator=g).to(dtype)
+    out = rlt.attend_paged(q.cuda(), cache, table, i32(0, m), i32(L), m, L).double().cpu()
+    ref, _, mass, size = attend64(q.double(), held, L, 0)
+    assert ((out - ref).abs() <= attend_bound(ref, mass, size, dh, dtype)).all()
+
+
+def test_a_first_call_may_be_captured():
+    """In a process of its own: nothing of the library has run before the capture."""
+    code = '''
+import torch
+from token_recurrent_decoding_b200 import rlt
+cache = rlt.PagedKV.empty(8, 16, 2, 64, torch.bfloat16, rlt.KV_E4M3)
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+table, cu, n = torch.arange(8, device="cuda").int()[None], i32(0, 40), i32(100)
+x = torch.randn(40, 4, 64, device="cuda").bfloat16()
+out = torch.zeros_like(x)
+t = torch.randn(2, 3, 500, device="cuda")
+u = torch.rand(2, 3, device="cuda")
+d = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+work = torch.empty(rlt.attend_paged_workspace_bytes(cache, 1, 4, 40, 40, 100), dtype=torch.uint8,
+                   device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    rlt.paged_append(cache, table, x[:, :2], x[:, 2:], cu, n)
+    rlt.attend_paged(x, cache, table, cu, n, 40, 100, out=out, workspace=work)
+    tokens, counts = rlt.verify(t, t[:, :2], d, 1.0, u)
+cache.pages.view(torch.uint8).zero_()
+cache.scales.fill_(127)
+graph.replay()
+torch.cuda.synchronize()
+want = rlt.attend_paged(x, cache, table, cu, n, 40, 100)
+assert torch.equal(out, want) and torch.isfinite(out.float()).all() and (counts >= 1).all()
+print("fine")
+'''
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]

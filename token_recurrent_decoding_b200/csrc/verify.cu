@@ -35,6 +35,11 @@
 // entries and the exponent field, 2^(f / 256) from the exponential series to
 // the third power, whose next term is below (ln 2 / 512)^4 / 24 = 1.4e-13.
 // Weights below 2^-1000 are nothing.
+//
+// Measured on a B200: 64 sequences, up to 5 drafts, 131072 words 97 us
+// (k_verify_rows 33 us, 0.92 of the copy rate; k_verify_draw 64 us, bound by
+// the latency and rate of fp64 operations); 2 sequences of 4 drafts, 32768
+// words 18 us.
 #include <cmath>
 
 #include "paged.cuh"
