@@ -29,7 +29,7 @@
 // k_pattn_merge.
 //
 // Measured on a B200 (device time): one step of 32 sequences of 2000-4096 keys,
-// 16 heads of 128, 8 bits 134 us (3.1 TB/s: bound by issue, about 700
+// 16 heads of 128, 8 bits 134-142 us (3 TB/s: bound by issue, about 700
 // instructions per 16 keys and head, half of them turning codes into bf16);
 // five tokens of 48 sequences of 1000-8192 keys, 32 heads on 8 key heads of
 // 128, bf16 253 us (3.6 TB/s: latency at 8 warps an SM, O of 32 rows takes 128
