@@ -418,6 +418,29 @@ def test_pages_behind_four_gigabytes(kind, m):
     assert ((out - ref).abs() <= attend_bound(ref, mass, size, dh, dtype)).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32", "bf16e4"])
+def test_the_largest_batch(kind):
+    """2048 sequences: the plan at its largest beside the largest tiles in shared memory; empty ones,
+    one with enough rows for 128-row tiles, one with enough keys for splits."""
+    n = 2048
+    rows = [(i * 7) % 3 for i in range(n)]
+    lens = [r + (i * 5) % 4 for i, r in enumerate(rows)]
+    rows[1000], lens[1000] = 45, 60
+    rows[2047], lens[2047] = 1, 700
+    c = Case(rows, lens, H=1, dh=128, page=16, dtype=F32 if kind == "f32" else BF16,
+             e4=kind.endswith("e4"), seed=13, pad=1).device()
+    _check(c, 1)
+    k = torch.zeros((c.total, 1, 128), dtype=c.dtype, device="cuda")
+    rlt.paged_append(c.cache, c.d_table, k, k, c.d_cu, c.d_len)
+    out, out2 = torch.ones_like(k), torch.ones_like(k)
+    rlt.paged_read(c.cache, c.d_table, c.d_cu, c.d_len, out, out2)
+    assert (out[:-1] == 0).all() and (out[-1] == 1).all() and (out2[:-1] == 0).all()
+    bad = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(rlt.RLTError):
+        rlt.paged_read(c.cache, torch.zeros((n + 1, 1), dtype=torch.int32, device="cuda"),
+                       torch.zeros(n + 2, dtype=torch.int32, device="cuda"), bad, out, out2)
+
+
 def test_a_first_call_may_be_captured():
     """In a process of its own: nothing of the library has run before the capture."""
     code = '''
