@@ -1,0 +1,78 @@
+"""The paged cache and the attention over it where values stop being finite, at the ends of their
+types and at the ends of the arguments' ranges: on the GPU, against float64 on the CPU."""
+import math
+
+import pytest
+import torch
+
+from paged_cases import BF16, F32, Case, attend64, attend_bound
+from token_recurrent_decoding_b200 import rlt
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["bf16", "f32", "bf16e4", "f32e4"]
+
+
+def _case(kind, rows, lens, **kw):
+    return Case(rows, lens, dtype=F32 if kind[0] == "f" else BF16, e4=kind.endswith("e4"), **kw)
+
+
+def _place(c, b, pos):
+    return int(c.table[b, pos // c.page]), pos % c.page
+
+
+def _spoil(c, b, head, kv, pos, value):
+    """The whole key or value of one position and head becomes `value` (8 bits: NaN)."""
+    pg, sl = _place(c, b, pos)
+    if c.e4:
+        c.scales[pg, head, kv, sl] = 255
+        c.pages.view(torch.uint8)[pg, head, kv, sl] = 0
+    else:
+        c.pages[pg, head, kv, sl] = value
+
+
+def _sees(c, b, pos, window):
+    """[m] whether row i of sequence b sees key `pos`."""
+    p = c.lens[b] - c.rows[b] + torch.arange(c.rows[b])
+    return (pos <= p) & ((pos > p - window) if window else torch.ones_like(p, dtype=torch.bool))
+
+
+# (8 bits hold a NaN only: an infinity is stored as one)
+@pytest.mark.parametrize("kind,value", [(k, math.nan) for k in KINDS] +
+                         [("bf16", math.inf), ("f32", math.inf)])
+@pytest.mark.parametrize("m,before,group,dh,window", [
+    (256, 0, 1, 64, 0), (256, 0, 1, 128, 0), (300, 37, 1, 64, 0), (130, 0, 2, 128, 0),
+    (150, 21, 3, 64, 0), (300, 0, 1, 64, 140), (256, 200, 2, 64, 90), (257, 5, 1, 128, 128)])
+def test_rows_that_see_a_value_that_is_not_finite(kind, value, m, before, group, dh, window):
+    """Wherever it lies among the tiles and whichever other rows see it: those rows are not finite
+    (NaN from a NaN), all others are as without it."""
+    L = m + before
+    c = _case(kind, [m], [L], H=2, dh=dh, page=32, seed=m + group).device()
+    q = c.queries(2 * group)
+    dq = q.cuda()
+    clean = c.pages.clone(), None if c.scales is None else c.scales.clone()
+    held, seen = c.kv[0].clone(), 0
+    for pos in (5, 100, 127, 128, 200, L - 2):
+        if pos >= L:
+            continue
+        c.pages.copy_(clean[0])
+        if c.e4:
+            c.scales.copy_(clean[1])
+        _spoil(c, 0, 1, 1, pos, value)
+        c.device()
+        c.kv[0] = held.clone()
+        c.kv[0][pos, 1, 1] = 0.0
+        lse = torch.zeros((m, 2 * group), device="cuda")
+        out = rlt.attend_paged(dq, c.cache, c.d_table, c.d_cu, c.d_len, m, L, lse=lse,
+                               window=window).double().cpu()
+        ref, _, mass, size = attend64(q.double(), c.kv[0], L, window)
+        hit = torch.zeros((m, 2 * group), dtype=torch.bool)
+        hit[:, group:] = _sees(c, 0, pos, window)[:, None]
+        seen += int(hit.any())
+        assert not torch.isfinite(out[hit]).any(), pos
+        if value != value:
+            assert torch.isnan(out[hit]).all(), pos
+        bound = attend_bound(ref, mass, size, dh, c.dtype)
+        assert ((out - ref).abs()[~hit] <= bound[~hit]).all(), pos
+        assert torch.isfinite(lse.cpu()[~hit]).all(), pos
+    assert seen > 0

@@ -654,8 +654,10 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
           }
         }
         const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
+        // the loaders judge by the whole item: what they cleared counts here too
+        // where this half sees the tile whole
         const bool all = pw_all_see(A, I, key0, pos_lo, pos_hi) &&
-                         !(fl[0] | fl[1] | fl[2] | fl[3]);
+                         !(fl[0] | fl[1] | fl[2] | fl[3] | fl[4] | fl[5] | fl[6] | fl[7]);
         // the row of scores and its maximum
         uint32_t s[128];
 #pragma unroll
