@@ -76,3 +76,64 @@ def test_rows_that_see_a_value_that_is_not_finite(kind, value, m, before, group,
         assert ((out - ref).abs()[~hit] <= bound[~hit]).all(), pos
         assert torch.isfinite(lse.cpu()[~hit]).all(), pos
     assert seen > 0
+
+
+# ------------------------------------------------------------------ other streams
+def _pool_of(t):
+    """The stream whose memory t lies in."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def _calls(c, side):
+    """The calls that make their own buffers, on `side`, with what they give on the current stream."""
+    q = c.queries(4).cuda()
+    t = torch.randn((64, 3, 5000), device="cuda")
+    x = torch.zeros((64, 2), dtype=torch.int32, device="cuda")
+    u = torch.full((64, 3), 0.5, device="cuda")
+    attend = lambda s: (rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, c.d_len, 40,  # noqa: E731
+                                         3000, stream=s),)
+    verify = lambda s: rlt.verify(t, t[:, :2], x, 1.0, u, stream=s)  # noqa: E731
+    wants = [f(None) for f in (attend, verify)]
+    torch.cuda.synchronize()
+    return [(lambda: attend(side), wants[0]), (lambda: verify(side), wants[1])]
+
+
+def test_buffers_of_a_call_on_another_stream_are_that_streams_own():
+    c = _case("bf16", [1, 40], [3000, 900], H=2, dh=64, page=64, seed=1).device()
+    side = torch.cuda.Stream()
+    for call, want in _calls(c, side):
+        got = call()
+        assert all(_pool_of(t) == side.cuda_stream for t in got)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # on the current stream, named or not, nothing changes
+    here = torch.cuda.current_stream()
+    for stream in (None, here):
+        for call, _ in _calls(c, stream):
+            assert all(_pool_of(t) == here.cuda_stream for t in call())
+
+
+def test_a_call_on_another_stream_leaves_pending_work_alone():
+    """Work of the current stream is still to read blocks that were freed behind it, of every size
+    the calls may want, while they run on another stream."""
+    c = _case("bf16", [1, 40], [3000, 900], H=2, dh=64, page=64, seed=1).device()
+    side = torch.cuda.Stream()
+    a = torch.randn((4096, 4096), device="cuda")
+    for call, want in _calls(c, side):
+        sizes = [2 ** i for i in range(9, 25)]
+        kept = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        blocks = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a @ a  # a few milliseconds
+        for to, block in zip(kept, blocks):
+            to.copy_(block)
+        del blocks, block
+        got = call()
+        torch.cuda.synchronize()
+        assert all((to == 7).all() for to in kept)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))

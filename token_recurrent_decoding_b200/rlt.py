@@ -280,10 +280,21 @@ def _launch(dev: int, stream, what: str, fn, *args):
         _check(rc, what)
 
 
-def _own(stream, t):
-    """t, made for a call on `stream`, kept from reuse until that stream has passed the call."""
-    if stream is not None:
-        t.record_stream(stream)
+def _empty(stream, device, shape, dtype, returned=False):
+    """A tensor for a call on `stream` (None: the device's current one), from that stream's own
+    memory: a block of the current stream's may still be in use there by work that it was freed
+    behind. One that is handed back to the caller is kept from reuse until the current stream has
+    passed what the caller does with it there."""
+    torch = _torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream == stream.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
     return t
 
 
@@ -405,8 +416,7 @@ def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_l
     if ldq < 0:
         _bad(what + ": q [rows][n_heads][head_dim] of the cache's dtype")
     if out is None:
-        out = _own(stream, torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype,
-                                       device=cache.device))
+        out = _empty(stream, cache.device, (rows, heads, cache.head_dim), cache.dtype, True)
     ldo = cache._stride(out, heads)
     if ldo < 0 or out.size(0) != rows:
         _bad(what + ": out of q's shape and dtype")
@@ -418,9 +428,8 @@ def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_l
     if r is None:
         _bad(what + ": " + _ROWS)
     if workspace is None:
-        workspace = _own(stream, torch.empty(
-            attend_paged_workspace_bytes(cache, r.n, heads, rows, max_rows, max_len),
-            dtype=torch.uint8, device=cache.device))
+        workspace = _empty(stream, cache.device, attend_paged_workspace_bytes(
+            cache, r.n, heads, rows, max_rows, max_len), torch.uint8)
     elif not (workspace.dtype is torch.uint8 and workspace.is_contiguous()
               and workspace.get_device() == dev):
         _bad(what + ": workspace uint8 on the cache's GPU")
@@ -466,16 +475,15 @@ def verify(target, draft, draft_tokens, temperature: float, uniforms=None, draft
     if draft_lengths is not None and not _ints(draft_lengths, dev, n):
         _bad(what + ": draft_lengths int32 [n]")
     if tokens is None:
-        tokens = _own(stream, torch.empty((n, k + 1), dtype=torch.int32, device=target.device))
+        tokens = _empty(stream, target.device, (n, k + 1), torch.int32, True)
     elif not fits(tokens, torch.int32, k + 1):
         _bad(what + ": tokens int32 [n][k + 1]")
     if counts is None:
-        counts = _own(stream, torch.empty(n, dtype=torch.int32, device=target.device))
+        counts = _empty(stream, target.device, n, torch.int32, True)
     elif not _ints(counts, dev, n):
         _bad(what + ": counts int32 [n]")
     if workspace is None:
-        workspace = _own(stream, torch.empty(verify_workspace_bytes(n, k, V), dtype=torch.uint8,
-                                             device=target.device))
+        workspace = _empty(stream, target.device, verify_workspace_bytes(n, k, V), torch.uint8)
     elif not (workspace.dtype is torch.uint8 and workspace.is_contiguous()
               and workspace.get_device() == dev):
         _bad(what + ": workspace uint8 on the logits' GPU")
