@@ -137,3 +137,38 @@ def test_a_call_on_another_stream_leaves_pending_work_alone():
         torch.cuda.synchronize()
         assert all((to == 7).all() for to in kept)
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# -------------------------------------------------------- the ends of the types
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [3, 150])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_the_largest_numbers_in_unseen_places_do_not_matter(kind, m, window, sign):
+    """Keys and values of the type's largest or lowest value that only the last row sees."""
+    L = m + 30
+    c = _case(kind, [m], [L], H=1, dh=64, page=16, seed=3)
+    for kv in (0, 1):
+        _spoil(c, 0, 0, kv, L - 1, sign * torch.finfo(c.dtype).max)
+    c.device()
+    q = c.queries(2)
+    out = rlt.attend_paged(q.cuda(), c.cache, c.d_table, c.d_cu, c.d_len, m, L,
+                           window=window).double().cpu()
+    ref, _, mass, size = attend64(q.double(), c.kv[0], L, window)
+    assert ((out - ref).abs() <= attend_bound(ref, mass, size, 64, c.dtype))[:-1].all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [16, 32, 64, 128])
+def test_the_largest_numbers_are_values_like_others(kind, dh):
+    """One key: its weight is one, so its value comes out, to the two roundings of the division."""
+    c = _case(kind, [1], [1], H=1, dh=dh, page=16, seed=3)
+    top = torch.finfo(c.dtype).max
+    c.pages[:, :, 1] = top
+    c.pages[:, :, 1, :, ::2] = -top
+    c.device()
+    q = c.queries(1)
+    out = rlt.attend_paged(q.cuda(), c.cache, c.d_table, c.d_cu, c.d_len, 1, 1).double().cpu()
+    want = torch.full((dh,), top, dtype=torch.float64)
+    want[::2] = -top
+    assert ((out[0, 0] - want).abs() <= 2.0 ** -23 * top).all()

@@ -289,16 +289,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-// (a, b) as P pairs of bf16 whose sum is the pair to 8 * P bits.
+// (a, b) as bf16 to nearest; what lies beyond bf16's largest becomes that.
+__device__ __forceinline__ uint32_t pack_bf16_finite(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+// (a, b) as P pairs of bf16 whose sum is the pair to 8 * P bits. Of several parts
+// the first is kept finite: fp32 values above bf16's largest (3.39e38) would round
+// to an infinity, which a weight of zero turns into NaN for rows that do not see
+// the key. Infinities and NaN reach the last part as NaN.
 template <int P> __device__ __forceinline__ void split_pair(float a, float b, uint32_t out[P]) {
 #pragma unroll
   for (int i = 0; i < P; i++) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    out[i] = *reinterpret_cast<const uint32_t *>(&v);
+    if (P > 1 && i == 0) {
+      out[i] = pack_bf16_finite(a, b);
+    } else {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+      out[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
     if (i + 1 < P) {
-      const float2 f = __bfloat1622float2(v);
-      a -= f.x;
-      b -= f.y;
+      a -= __uint_as_float(out[i] << 16);
+      b -= __uint_as_float(out[i] & 0xffff0000u);
     }
   }
 }
