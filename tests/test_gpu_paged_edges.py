@@ -172,3 +172,30 @@ def test_the_largest_numbers_are_values_like_others(kind, dh):
     want = torch.full((dh,), top, dtype=torch.float64)
     want[::2] = -top
     assert ((out[0, 0] - want).abs() <= 2.0 ** -23 * top).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m", [2, 40, 150])
+@pytest.mark.parametrize("size", [1e4, 1e9, 1e13, 1e36])
+def test_scores_far_beyond_the_exponent(kind, m, size):
+    """Scores of up to 1e36, finite in fp32: one key takes nearly every row, whatever the spacing of
+    fp32 there is (the scores are single products, so that no order of a sum decides)."""
+    L, dh = m + 70, 64
+    c = _case(kind, [m], [L], H=1, dh=dh, page=16, seed=4).device()
+    q = c.queries(2) * math.sqrt(size)
+    q[:, :, 1:] = 0
+    if not c.e4:
+        c.d_pages[:, :, 0] *= math.sqrt(size)
+        c.kv[0][:, :, 0] = (c.kv[0][:, :, 0].to(c.dtype).cuda() * math.sqrt(size)).double().cpu()
+    lse = torch.zeros((m, 2), device="cuda")
+    out = rlt.attend_paged(q.cuda(), c.cache, c.d_table, c.d_cu, c.d_len, m, L,
+                           lse=lse).double().cpu()
+    ref, rl, mass, size = attend64(q.double(), c.kv[0], L, 0)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    # a score's own roundings, as attend_bound counts them, and where they leave the winner open
+    # (another key within them), any mean of values
+    bound = attend_bound(ref, mass, size, dh, c.dtype)
+    top = c.kv[0][:, 0, 1].abs().max() * 2
+    assert ((out - ref).abs() <= bound.clamp(max=top)).all()
+    lb = size * (dh + 8) * 2.0 ** -23 + 512 * 2.0 ** -23 + rl.abs() * 2.0 ** -22
+    assert ((lse.double().cpu() - rl).abs() <= lb).all()

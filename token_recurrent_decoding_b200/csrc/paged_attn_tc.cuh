@@ -611,6 +611,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = tmem + 256 + t * DH + ((uint32_t)((warp & 3) * 32) << 16);
+    const float lift = 8.f / A.scale_log2;
     uint32_t n_tile = 0, n_t = 0, n_item = 0;
     bool ok = true;
     for (int it = blockIdx.x; ok && it < total; it += gridDim.x) {
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         n_tile += I.nk;
         continue;
       }
-      float m = -INFINITY, l = 0.f;
+      float top_score = -INFINITY, l = 0.f;  // the reference, not scaled; the sum
       for (int i = from; !idle && i < I.nk; i += by) {
         const int st = (n_tile + i) % ST, use = (n_tile + i) / ST;
         const int key0 = I.k0 + i * PW_TK;
@@ -683,11 +684,10 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         for (int e = 0; e < 128; e += 2)
           mxs[(e >> 1) & 3] = max3(mxs[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
-        mx *= A.scale_log2;
         // O keeps its reference until the maximum has outgrown it by 2^8
-        const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+        const bool grow = mx > top_score + lift || (top_score == -INFINITY && mx > top_score);
         if (i > from && __any_sync(FULL_MASK, grow)) {
-          const float corr = grow ? pa_exp2(m - mx) : 1.f;
+          const float corr = grow ? pa_exp2((top_score - mx) * A.scale_log2) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < DH / 16; c++) {
             float v[16];
@@ -700,9 +700,18 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
           pw_wait_st();
           l *= corr;
         }
-        if (grow) m = mx;
-        const float base = m == -INFINITY ? 0.f : m;
-        const float2 sc2 = make_float2(A.scale_log2, A.scale_log2), nb2 = make_float2(-base, -base);
+        if (grow) top_score = mx;
+        // A weight's argument is score * scale - base, one multiply-add: the product
+        // is not rounded, the base was, so all weights of a row are off by the same
+        // 2^d, |d| half a unit in the base's last place, which the sum undoes. From
+        // 2^30 on 2^d could overflow, and neighbouring scores lie 2^-64 and more
+        // apart in weight: there the difference of the scores themselves does.
+        float sc = A.scale_log2, base = top_score == -INFINITY ? 0.f : top_score * A.scale_log2;
+        if (fabsf(base) >= 1073741824.f) {
+          sc = 1.f;
+          base = top_score;
+        }
+        const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
         // weights, packed in place: pair e of keys becomes s[e]. P is handed on
         // in two parts, 96 keys and 32, so that most of PV runs under the last
         // exponentials; stores are waited for a few pairs after their issue.
@@ -752,6 +761,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
       }
       n_tile += I.nk;
       const bool on = r < I.R;
+      const float m = top_score * A.scale_log2;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float *part = A.part + ((size_t)P.parts[I.b] + ((size_t)tok * A.heads + head) * I.S.splits +
                               (I.S.streams ? 2 * I.range + t : I.range)) * (DH + 2);
