@@ -532,11 +532,12 @@ RLT_API int rlt_attend_noalloc(const float *q, const void *kv, const int32_t *h_
  *           for 2^(b - 127), an element's value is e4m3 * 2^(b - 127). Writing
  *           takes the least power of two >= 2^-110 with max|x| <= 448 * 2^e, so
  *           x * 2^-e is exact, each element is rounded once (to nearest, ties to
- *           even), and what is stored is exact in bf16 and fp32. A block that
- *           holds an infinity or a NaN is stored as NaN: zeros under scale byte
- *           255. The element codes of NaN (0x7f, 0xff) are not written; in pages
- *           from elsewhere they stand for +-480. Scale bytes from elsewhere: 17..187
- *           or 255. */
+ *           even), and what is stored is exact in bf16 and fp32; elements that
+ *           would round to 2^128 (magnitudes from 248 * 2^120 = 3.30e38 on) become
+ *           240 * 2^120. A block that holds an infinity or a NaN is stored as NaN:
+ *           zeros under scale byte 255. The element codes of NaN (0x7f, 0xff) are not
+ *           written; in pages from elsewhere they stand for +-480. Scale bytes from
+ *           elsewhere: 17..246 or 255. */
 enum { RLT_KV_PLAIN = 0, RLT_KV_E4M3 = 1 };
 typedef struct rlt_paged_kv {
   void *pages;

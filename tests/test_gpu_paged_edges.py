@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from paged_cases import BF16, F32, Case, attend64, attend_bound
+from paged_cases import BF16, F32, Case, attend64, attend_bound, quantised
 from token_recurrent_decoding_b200 import rlt
 
 pytestmark = pytest.mark.gpu
@@ -199,3 +199,37 @@ def test_scores_far_beyond_the_exponent(kind, m, size):
     assert ((out - ref).abs() <= bound.clamp(max=top)).all()
     lb = size * (dh + 8) * 2.0 ** -23 + 512 * 2.0 ** -23 + rl.abs() * 2.0 ** -22
     assert ((lse.double().cpu() - rl).abs() <= lb).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dh", [16, 64])
+@pytest.mark.parametrize("m", [3, 150])
+def test_the_largest_numbers_in_8_bits(dtype, dh, m):
+    """What is written from finite numbers reads back finite: from 248 * 2^120 on, where the nearest
+    element would be 2^128, as 240 * 2^120. Rows that do not see them are as without them."""
+    L, top = m + 30, torch.finfo(dtype).max
+    c = Case([m], [L], H=2, dh=dh, page=16, seed=3, dtype=dtype, e4=True)
+    x = torch.randn((m, 4, dh), generator=c.g).to(dtype)
+    edges = torch.tensor([top, -top, 248 * 2.0 ** 120, -249 * 2.0 ** 120, 240 * 2.0 ** 120,
+                          247 * 2.0 ** 120, 2.0 ** 127, 1.0], dtype=torch.float64).to(dtype)
+    x[-1, :, :] = edges.repeat(dh // 8)
+    x[0, 0] = 447 * 2.0 ** 119  # the first head's key, under the scale below: 448 * 2^119
+    c.device()
+    dx = x.cuda()
+    rlt.paged_append(c.cache, c.d_table, dx[:, :2], dx[:, 2:], c.d_cu, c.d_len)
+    ko, vo = (torch.empty((m, 2, dh), dtype=dtype, device="cuda") for _ in range(2))
+    rlt.paged_read(c.cache, c.d_table, c.d_cu, c.d_len, ko, vo)
+    want = torch.from_numpy(quantised(x.double().numpy())[0])
+    assert (want.abs() >= 2.0 ** 128).any()
+    want = want.clamp(-240 * 2.0 ** 120, 240 * 2.0 ** 120)
+    got = torch.cat([ko, vo], 1).double().cpu()
+    assert torch.isfinite(got).all() and torch.equal(got, want)
+    held = c.kv[0].clone()
+    held[L - m:] = torch.stack([want[:, :2], want[:, 2:]], 2)
+    q = c.queries(2) / 64
+    q[:, :, 1:] = 0  # scores of the largest keys stay finite
+    out = rlt.attend_paged(q.cuda(), c.cache, c.d_table, c.d_cu, c.d_len, m, L).double().cpu()
+    ref, _, mass, size = attend64(q[1:].double(), held, L, 0)
+    assert torch.isfinite(out[:-1]).all()
+    ok = attend_bound(ref, mass, size, dh, dtype)
+    assert ((out[1:-1, 1] - ref[:-1, 1]).abs() <= ok[:-1, 1]).all()

@@ -17,6 +17,7 @@ namespace rlt {
 
 constexpr float E4M3_MAX = 448.f;
 constexpr int E4M3_EMIN = -110;  // keeps every stored value a normal bf16
+constexpr int E4M3_EMAX = 120;   // of the largest finite numbers: 2^128 > 448 * 2^119
 
 struct PagedView {
   uint8_t *pages;

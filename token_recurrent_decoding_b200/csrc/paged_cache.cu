@@ -55,7 +55,9 @@ template <int N> __device__ __forceinline__ void store_row(bf16 *p, const float 
 }
 
 // N elements as e4m3 under a scale shared by LANES neighbouring lanes; returns
-// the scale byte. The lanes of a block are all active.
+// the scale byte. The lanes of a block are all active. Under the largest scale,
+// 2^120, elements from 248 * 2^120 on would round to 2^128, an infinity in fp32
+// and bf16: they become 240 * 2^120, the largest below.
 template <int N, int LANES>
 __device__ __forceinline__ int quantise(const float f[N], uint32_t w[N / 4]) {
   // magnitudes as bits: ordered like the values, infinities and NaN above all
@@ -79,6 +81,11 @@ __device__ __forceinline__ int quantise(const float f[N], uint32_t w[N / 4]) {
     const float2 y = make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv);
     w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3) |
            ((uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << 16);
+  }
+  if (e == E4M3_EMAX) {  // codes 0x78 (256) become 0x77 (240)
+#pragma unroll
+    for (int i = 0; i < N / 4; i++)
+      w[i] = __vminu4(w[i] & 0x7f7f7f7fu, 0x77777777u) | (w[i] & 0x80808080u);
   }
   return e + 127;
 }
