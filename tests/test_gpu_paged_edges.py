@@ -233,3 +233,18 @@ def test_the_largest_numbers_in_8_bits(dtype, dh, m):
     assert torch.isfinite(out[:-1]).all()
     ok = attend_bound(ref, mass, size, dh, dtype)
     assert ((out[1:-1, 1] - ref[:-1, 1]).abs() <= ok[:-1, 1]).all()
+
+
+# ------------------------------------------------- the ends of the arguments' ranges
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m", [5, 100])
+def test_the_largest_windows_hide_nothing(kind, m):
+    """Also where the first rows lie before position 0."""
+    c = _case(kind, [m], [m], H=1, dh=64, page=16, seed=3).device()
+    q = c.queries(2).cuda()
+    short = c.d_len - 3
+    want = rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, short, m, m)
+    assert (want[:3] == 0).all() and (want[3:] != 0).any()
+    for window in (m - 3, m, m + 1, 2 ** 31 - 1):
+        got = rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, short, m, m, window=window)
+        assert torch.equal(got, want), window

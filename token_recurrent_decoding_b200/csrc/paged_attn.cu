@@ -169,7 +169,9 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
   A.group = n_heads / c->n_kv_heads;
   A.max_rows = max_rows;
   A.max_len = max_len;
-  A.window = window;
+  // positions are below max_len: a window of that or more hides nothing (and what
+  // is left cannot overflow from rows before position 0)
+  A.window = window < max_len ? window : 0;
   A.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->head_dim));
   A.part = static_cast<float *>(workspace);
   A.part_rows = (int)parts;
