@@ -12,46 +12,9 @@ namespace {
 bool wide_kernel(const rlt_paged_kv *c) {
   return c->dtype == RLT_BF16 && (c->head_dim == 64 || c->head_dim == 128);
 }
-// Whether a sequence within this bound may go to k_pattn_wide.
-bool may_be_wide(const rlt_paged_kv *c, int n_heads, int max_rows) {
-  return wide_kernel(c) && (int64_t)max_rows * (n_heads / c->n_kv_heads) >= PA_WIDE_FROM;
-}
-
-int64_t most_splits(int max_len, int min_keys) {
-  const int64_t n = ((int64_t)max_len + PA_TK + min_keys - 1) / min_keys;
-  return n < PA_MAX_SPLITS ? n : PA_MAX_SPLITS;
-}
-
-// Partial rows the split rule can make, at most. k_pattn: a sequence of m rows
-// makes m * heads * splits, with splits below units aimed at / own units + 1 and
-// own units at least m * heads / rows of a unit. k_pattn_wide: the same for
-// tiles; streams: two slices a range of at most PA_STREAM_ROWS rows a kv head.
-int64_t partial_rows(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows,
-                     int max_len) {
-  const int64_t cells = (int64_t)rows * n_heads, narrow = most_splits(max_len, PA_MIN_KEYS);
-  int64_t most = narrow > 1 ? (int64_t)n * PA_SPLIT_UNITS * PA_UNIT_ROWS + cells : 0;
-  if (most > narrow * cells) most = narrow * cells;
-  if (wide_kernel(c) && most > 0) {
-    // only few rows are left to k_pattn
-    const int64_t few = (int64_t)n * PA_WIDE_FROM * c->n_kv_heads * narrow;
-    if (most > few) most = few;
-  }
-  if (may_be_wide(c, n_heads, max_rows)) {
-    const int64_t wide = most_splits(max_len, PA_WIDE_KEYS),
-                  streams = 2 * most_splits(max_len, PA_STREAM_KEYS);
-    int64_t a = 0, b = streams * cells;
-    if (wide > 1) {
-      // (sequences of more than PA_STREAM_ROWS stacked rows)
-      int64_t seqs = (int64_t)rows * (n_heads / c->n_kv_heads) / PA_STREAM_ROWS;
-      if (seqs > n) seqs = n;
-      a = seqs * PA_WIDE_UNITS * PA_WIDE_ROWS + cells;
-      if (a > wide * cells) a = wide * cells;
-    }
-    const int64_t few = (int64_t)n * PA_STREAM_ROWS * c->n_kv_heads * streams;
-    if (b > few) b = few;
-    most += a + b;
-  }
-  return most;
+int64_t partial_rows_of(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows,
+                        int max_len) {
+  return partial_rows(wide_kernel(c), c->n_kv_heads, n, n_heads, rows, max_rows, max_len);
 }
 
 bool attn_shape_ok(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_rows, int max_len) {
@@ -59,7 +22,7 @@ bool attn_shape_ok(const rlt_paged_kv *c, int n, int n_heads, int rows, int max_
          n_heads <= 1024 && n_heads % c->n_kv_heads == 0 && rows >= 0 && max_rows >= 0 &&
          max_len >= 0 && max_len <= (1 << 28) && (int64_t)rows * n_heads <= (1 << 28) &&
          (int64_t)max_rows * n_heads <= (1 << 28) &&
-         partial_rows(c, n, n_heads, rows, max_rows, max_len) <= (1 << 30);
+         partial_rows_of(c, n, n_heads, rows, max_rows, max_len) <= (1 << 30);
 }
 
 size_t workspace_bytes_of(int dh, int64_t part_rows) {
@@ -139,7 +102,7 @@ RLT_API size_t rlt_attend_paged_workspace_bytes(const rlt_paged_kv *cache, int n
                                                 int rows, int max_rows, int max_len) {
   if (!attn_shape_ok(cache, n, n_heads, rows, max_rows, max_len)) return 0;
   return workspace_bytes_of(cache->head_dim,
-                            partial_rows(cache, n, n_heads, rows, max_rows, max_len));
+                            partial_rows_of(cache, n, n_heads, rows, max_rows, max_len));
 }
 
 RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, const void *q,
@@ -155,7 +118,7 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
       !dense_rows_ok(out, ldo, n_heads, c->head_dim, c->dtype) || !workspace ||
       ((uintptr_t)workspace & 255) || ((uintptr_t)lse & 3))
     return RLT_ERR_INVALID_ARG;
-  const int64_t parts = partial_rows(c, w->n, n_heads, w->rows, max_rows, max_len);
+  const int64_t parts = partial_rows_of(c, w->n, n_heads, w->rows, max_rows, max_len);
   if (workspace_bytes < workspace_bytes_of(c->head_dim, parts)) return RLT_ERR_CAPACITY;
   AttnArgs A;
   A.C = paged_view(c);
@@ -187,7 +150,7 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
     e = e4 ? launch_attn<PA_E4M3>(A, dh, sms, st) : launch_attn<PA_BF16>(A, dh, sms, st);
   else
     e = e4 ? launch_attn<PA_E4M3_F32>(A, dh, sms, st) : launch_attn<PA_F32>(A, dh, sms, st);
-  if (e == cudaSuccess && may_be_wide(c, n_heads, max_rows))
+  if (e == cudaSuccess && may_be_wide(A.wide, c->n_kv_heads, n_heads, max_rows))
     e = launch_wide(A, e4, dh, sms, st);
   if (e == cudaSuccess && parts > 0)
     e = c->dtype == RLT_BF16 ? launch_merge<bf16>(A, dh, sms, st)

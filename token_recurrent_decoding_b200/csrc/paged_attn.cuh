@@ -39,74 +39,11 @@
 #include <type_traits>
 
 #include "paged.cuh"
+#include "paged_plan.h"
 
 namespace rlt {
 
 constexpr int PA_THREADS = 128;
-constexpr int PA_TK = 16;            // keys of a tile
-constexpr int PA_UNIT_ROWS = 32;     // rows of a unit in the split rule
-constexpr int PA_SPLIT_UNITS = 256;  // units x splits aimed at per sequence
-constexpr int PA_MAX_SPLITS = 16;
-constexpr int PA_SHORT_SPLITS = 4;   // splits of ..
-constexpr int PA_MIN_KEYS = 256;     // .. at least so many keys, and more of ..
-constexpr int PA_LONG_KEYS = 2048;   // .. at least these
-constexpr int PA_ROW_BYTES = 64;     // keys x element bytes of a split for each row of a unit
-// The same of sequences that go to the tcgen05 kernel: tiles of 256 rows, one
-// CTA per SM, splits long enough that writing O in fp32 stays below a tenth.
-// Of sequences of at most PA_STREAM_ROWS rows both halves of a CTA take the same
-// rows and every other key tile (two streams, two slices of the split).
-constexpr int PA_WIDE_FROM = 33;     // rows from which a sequence goes there
-constexpr int PA_WIDE_ROWS = 256;
-constexpr int PA_WIDE_UNITS = 148;
-constexpr int PA_WIDE_KEYS = 4096;
-constexpr int PA_STREAM_ROWS = 128;
-constexpr int PA_STREAM_KEYS = 2048;
-
-// How one sequence is cut, from its own rows and length only.
-struct SeqCut {
-  int m, first;      // rows, position of the first
-  int k_lo, k_hi;    // keys any of its rows sees; k_lo is a multiple of 16
-  int ranges, keys;  // key ranges and keys of one (a multiple of 16)
-  int splits;        // slices its results come in: ranges, or two of each
-  bool wide, streams;
-};
-
-__device__ __host__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-__device__ __forceinline__ SeqCut cut_seq(int m, int len, int group, int kv_heads, int window,
-                                          bool wide_kernel, int es) {
-  SeqCut s;
-  s.m = m;
-  s.first = len - m;
-  s.k_hi = max(len, 0);
-  const int lo = window > 0 ? max(0, max(s.first, 0) - window + 1) : 0;
-  s.k_lo = min(lo, s.k_hi) & ~(PA_TK - 1);
-  const int span = s.k_hi - s.k_lo, rows = m * group;
-  s.wide = wide_kernel && rows >= PA_WIDE_FROM;
-  s.streams = s.wide && rows <= PA_STREAM_ROWS;
-  int n;
-  if (s.streams) {
-    n = span / PA_STREAM_KEYS;
-  } else if (s.wide) {
-    // a unit fills an SM: rounded down, as a second wave costs more than idle SMs
-    n = min(PA_WIDE_UNITS / (kv_heads * ceil_div(rows, PA_WIDE_ROWS)), ceil_div(span, PA_WIDE_KEYS));
-  } else {
-    const int units = max(1, kv_heads * ceil_div(rows, PA_UNIT_ROWS));
-    // Up to four ranges of 256 keys and more for the latency of few sequences;
-    // beyond that a range's own start and end (about 2 us) wants 2048 keys to
-    // pay: 32 steps in 8 bits of 2000-4096 positions took 169, 145, 135, 155 us
-    // with ranges of at least 256, 512, 1024, 2048. Writing and joining a slice
-    // stays below a tenth of reading its keys.
-    n = max(min(PA_SHORT_SPLITS, ceil_div(span, PA_MIN_KEYS)), ceil_div(span, PA_LONG_KEYS));
-    n = min(min(n, ceil_div(PA_SPLIT_UNITS, units)),
-            ceil_div(span, PA_ROW_BYTES / es * min(rows, PA_UNIT_ROWS)));
-  }
-  n = max(1, min(n, PA_MAX_SPLITS));
-  s.keys = max(PA_TK, ceil_div(ceil_div(span, n), PA_TK) * PA_TK);
-  s.ranges = max(1, ceil_div(span, s.keys));
-  s.splits = s.streams ? 2 * s.ranges : s.ranges;
-  return s;
-}
 
 struct AttnArgs {
   PagedView C;
