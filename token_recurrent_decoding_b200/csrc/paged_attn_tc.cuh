@@ -145,6 +145,15 @@ __device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
                : "memory");
 }
+// `times` arrivals of a thread where `on` holds, without a branch: the warp stays
+// together for the tensor-memory loads that follow.
+__device__ __forceinline__ void arrive_if(bool on, uint64_t *bar, int times) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %0, 0;\n"
+      " @p mbarrier.arrive.shared::cta.b64 _, [%1], %2;\n}\n" ::"r"((int)on),
+      "r"(smem_u32(bar)), "r"(times)
+      : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -647,13 +656,9 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
         // whose next scores are two tiles away, is given back by the issuer (a
         // commit a tile more took the other form from 579 to 694 us at 2048 rows
         // behind 30 thousand positions).
-        if (row == 0) {
-          const int times = by == 2 || I.R <= 128 ? 2 : 1;
-          for (int x = 0; x < times; x++) {
-            tc_mbar_arrive(k_empty + st);
-            if (by == 1 && i > 0) tc_mbar_arrive(v_empty + (n_tile + i - 1) % ST);
-          }
-        }
+        const int times = by == 2 || I.R <= 128 ? 2 : 1;
+        arrive_if(row == 0, k_empty + st, times);
+        arrive_if(row == 0 && by == 1 && i > 0, v_empty + (n_tile + i - 1) % ST, times);
         const uint32_t *fl = flags + ((n_tile + i) % Cfg::INFO) * 8;
         // the loaders judge by the whole item: what they cleared counts here too
         // where this half sees the tile whole
@@ -752,11 +757,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
           break;
         }
         tc_fence_after();
-        if (row == 0) {
-          tc_mbar_arrive(q_empty);
-          for (int x = 0; by == 1 && x < (I.R <= 128 ? 2 : 1); x++)
-            tc_mbar_arrive(v_empty + (n_tile + I.nk - 1) % ST);
-        }
+        arrive_if(row == 0, q_empty, 1);
+        arrive_if(row == 0 && by == 1, v_empty + (n_tile + I.nk - 1) % ST, I.R <= 128 ? 2 : 1);
         n_item++;
       }
       n_tile += I.nk;
@@ -776,13 +778,12 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
 #pragma unroll
           for (int e = 0; e < 32; e++) s[e] = 0;
         }
-        if (!on) continue;
-        if (I.S.splits > 1) {
+        if (on && I.S.splits > 1) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             *reinterpret_cast<float2 *>(part + 32 * c + e) =
                 make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-        } else {
+        } else if (on) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t w[4];
@@ -793,6 +794,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
             *reinterpret_cast<uint4 *>(dst + 32 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        __syncwarp();  // the warp loads O together
       }
       if (on) {
         if (I.S.splits > 1)
