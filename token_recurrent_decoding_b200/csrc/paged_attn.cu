@@ -140,7 +140,6 @@ RLT_API int rlt_attend_paged(const rlt_paged_kv *c, const rlt_paged_rows *w, con
   A.part_rows = (int)parts;
   A.wide = wide_kernel(c);
   A.es = c->kind == RLT_KV_E4M3 ? 1 : c->dtype == RLT_BF16 ? 2 : 4;
-  A.follows = 1;
   cudaStream_t st = (cudaStream_t)stream;
   const int sms = sm_count(), dh = c->head_dim;
   const bool e4 = c->kind == RLT_KV_E4M3;

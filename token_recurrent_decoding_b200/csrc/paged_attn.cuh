@@ -59,7 +59,6 @@ struct AttnArgs {
   int part_rows;
   int wide;          // whether k_pattn_wide takes part (its types and head sizes)
   int es;            // bytes of a cache element
-  int follows;       // k_pattn_wide: k_pattn of the same call runs before it
 };
 
 // What a block keeps of the call's sequences, in shared memory: 4 (n + 1) ints.

@@ -271,9 +271,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   }
   if (warp == 12) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
-  // behind k_pattn the predecessors' writes are complete (it waited before it
-  // let this kernel start) and its own are waited for at the end
-  if (!A.follows) pdl_wait();
+  // k_pattn of the same call runs before: its predecessors' writes are complete (it
+  // waited before it let this kernel start), its own are waited for at the end
   pdl_trigger();
   make_plan<PW_THREADS>(A, P, [&](const SeqCut &s) {
     return s.wide ? A.C.H * s.ranges * ceil_div(s.m * A.group, PW_RT) : 0;
@@ -811,7 +810,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) k_pattn_wide(const AttnArgs A) 
   __syncthreads();
   if (threadIdx.x == 0 && s_fail) flag_rows(A.R, RLT_PAGED_TIMEOUT);
   if (warp == 12) tmem_dealloc(tmem, 512);
-  if (A.follows) pdl_wait();
+  pdl_wait();
 }
 
 }  // namespace rlt
