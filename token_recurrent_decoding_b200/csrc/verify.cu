@@ -95,7 +95,8 @@ __device__ __noinline__ double weight_of(float x, float m, double per) {
 
 // The same for many logits of one row: the product of a logit is rounded once,
 // with the maximum's product, which all share, so rows whose products are too
-// large for that (and rows of infinities) take weight_of.
+// large for that take weight_of, and so do rows of infinities and temperatures
+// under which every finite logit weighs something (from about 5e35 on).
 struct RowWeights {
   float m, lo;   // what lies at or below lo weighs nothing
   double c, per256;
@@ -103,7 +104,8 @@ struct RowWeights {
 };
 __device__ __forceinline__ RowWeights row_weights(float m, double per) {
   const double per256 = 256.0 * per, c = (double)m * per256;
-  return {m, (float)((double)m - 1000.0 / per), c, per256, !isinf(m) && fabs(c) < 1073741824.0};
+  const float lo = (float)((double)m - 1000.0 / per);
+  return {m, lo, c, per256, !isinf(m) && !isinf(lo) && fabs(c) < 1073741824.0};
 }
 // Of plain rows; clamped to lo's (about 2^-1000) from below, NaN too.
 __device__ __forceinline__ double weight_fast(float x, const RowWeights &R, const double *table) {
