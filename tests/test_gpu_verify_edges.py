@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_verify import _compare, _inputs
+from test_gpu_verify import _compare, _inputs, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +20,21 @@ def test_the_highest_temperatures(tau, V):
     tau = float(torch.tensor(tau, dtype=torch.float32))
     _compare(t, d, x, tau, u)
     _compare(t, None, x, tau, u)
+
+
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_a_test_on_its_border_is_refused_whatever_the_logits_size(with_draft):
+    """p(x) = 1/2 exactly and u q(x) = 1/2: not below. The rows' sums are rounded with their largest
+    logit's product, which must not tell on one side only."""
+    n = 400
+    t = torch.full((n, 2, 8), -math.inf)
+    t[:, :, :2] = torch.linspace(1e5, 2.8e6, n)[:, None, None]
+    d = torch.full((n, 1, 8), -math.inf)
+    d[:, 0, 0] = torch.linspace(2.8e6, 1e5, n)
+    x = torch.zeros((n, 1), dtype=torch.long)
+    u = torch.full((n, 2), 0.5)
+    out, counts = _run(t, d if with_draft else None, x, 1.0, u)
+    assert (counts == 1).all() and (out[:, 0] == 1).all()
+    u[:, 0] = 0.5 - 2.0 ** -25  # the number below: accepted
+    out, counts = _run(t, d if with_draft else None, x, 1.0, u)
+    assert (counts == 2).all() and (out[:, 0] == 0).all()

@@ -70,6 +70,7 @@ struct VerifyArgs {
   const float *uniforms;
   int n, k, V, chunks;
   double per;    // log2(e) / temperature; 0: greedy
+  double reach;  // 1000 / per: what lies further below the maximum weighs nothing
   float per32;   // the same
   RowPart *parts;  // [n][2 k + 1][chunks]: target rows 0 .. k, then draft rows
   int *out, *counts;
@@ -102,9 +103,9 @@ struct RowWeights {
   double c, per256;
   bool plain;
 };
-__device__ __forceinline__ RowWeights row_weights(float m, double per) {
+__device__ __forceinline__ RowWeights row_weights(float m, double per, double reach) {
   const double per256 = 256.0 * per, c = (double)m * per256;
-  const float lo = (float)((double)m - 1000.0 / per);
+  const float lo = (float)((double)m - reach);
   return {m, lo, c, per256, !isinf(m) && !isinf(lo) && fabs(c) < 1073741824.0};
 }
 // Of plain rows; clamped to lo's (about 2^-1000) from below, NaN too.
@@ -124,6 +125,14 @@ __device__ __forceinline__ double weight_fast(float x, const RowWeights &R, cons
 // Whether a logit weighs anything in its row.
 __device__ __forceinline__ bool weighs(float x, const RowWeights &R) {
   return R.plain ? x > R.lo : x == x && x > -INFINITY && (!isinf(R.m) || x == R.m);
+}
+// A single logit's weight: the one the row's exact sums take it with. (The shared
+// rounding of the maximum's product, up to 2^-32.5 of every weight of the row,
+// then stands on both sides of a test.)
+__device__ __forceinline__ double weight_in_row(float x, const RowWeights &R, double per,
+                                                const double *table) {
+  if (!weighs(x, R)) return 0.0;
+  return R.plain ? weight_fast(x, R, table) : weight_of(x, R.m, per);
 }
 
 __device__ __forceinline__ double warp_sum64(double v) {
@@ -318,9 +327,10 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS,
   // The two sides of test i, u q(x) Zp < p(x) Zq, without Zp and Zq: every lane
   // of every block computes the same.
   auto sides = [&](int i, double &l, double &r) {
-    r = weight_of(s_lt[i], s_t[i].max, A.per);
+    r = weight_in_row(s_lt[i], row_weights(s_t[i].max, A.per, A.reach), A.per, table);
     l = (double)s_u[i];
-    if (DRAFT) l *= weight_of(s_ld[i], s_d[i].max, A.per);
+    if (DRAFT)
+      l *= weight_in_row(s_ld[i], row_weights(s_d[i].max, A.per, A.reach), A.per, table);
   };
   // Lowest index from `from` on that is not surely accepted (len: none); `close`
   // where the 32-bit sums do not decide it.
@@ -417,7 +427,7 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS,
       // exact sums of row j: they decide a close test, and a draw from the
       // difference needs them
       const RowSum T = s_t[j], D = DRAFT ? s_d[j] : RowSum{0.0, -INFINITY, 0};
-      const RowWeights P = row_weights(T.max, A.per), Q = row_weights(D.max, A.per);
+      const RowWeights P = row_weights(T.max, A.per, A.reach), Q = row_weights(D.max, A.per, A.reach);
       const float *tr = A.target + b * A.t_seq + j * A.t_pos;
       const float *dr = DRAFT ? A.draft + b * A.d_seq + j * A.d_pos : nullptr;
       const double ratio = DRAFT && D.sum > 0.0 ? T.sum / D.sum : 0.0;
@@ -501,8 +511,8 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS,
   const float *tr = A.target + b * A.t_seq + j * A.t_pos;
   const float *dr = DRAFT ? A.draft + b * A.d_seq + dj * A.d_pos : nullptr;
   const int skip = !DRAFT && A.k > 0 ? A.tokens[b * A.k + min(j, A.k - 1)] : -1;
-  const RowWeights P = row_weights(T.max, A.per);
-  const RowWeights Q = row_weights(DRAFT ? s_d[dj].max : -INFINITY, A.per);
+  const RowWeights P = row_weights(T.max, A.per, A.reach);
+  const RowWeights Q = row_weights(DRAFT ? s_d[dj].max : -INFINITY, A.per, A.reach);
   const double over = DRAFT && zq > 0.0 ? zp / zq : 0.0;  // the draft's weights on the target's scale
   const double point01 = (double)A.uniforms[(size_t)b * (A.k + 1) + A.k];
   bool residual = j < len;
@@ -667,6 +677,7 @@ RLT_API int rlt_verify(const float *target, int64_t target_seq, int64_t target_p
   A.V = vocab;
   A.chunks = verify_chunks(vocab);
   A.per = per;
+  A.reach = greedy ? 0.0 : 1000.0 / per;
   A.per32 = (float)(per < 3e38 ? per : 3e38);  // finite: zero differences stay zero
   A.parts = static_cast<RowPart *>(workspace);
   A.out = tokens;
