@@ -38,3 +38,18 @@ def test_a_test_on_its_border_is_refused_whatever_the_logits_size(with_draft):
     u[:, 0] = 0.5 - 2.0 ** -25  # the number below: accepted
     out, counts = _run(t, d if with_draft else None, x, 1.0, u)
     assert (counts == 2).all() and (out[:, 0] == 0).all()
+
+
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_logits_further_apart_than_the_type_reaches(with_draft):
+    """Logits of both signs near the type's ends, at a temperature where the lower ones weigh a tenth
+    of the upper ones: their difference is no finite number in 32 bits."""
+    n, V = 64, 40
+    g = torch.Generator().manual_seed(1)
+    t = torch.where(torch.rand((n, 2, V), generator=g) < 0.5, 3.3e38, -3.3e38)
+    t[:, :, 0] = 3.3e38
+    d = torch.where(torch.rand((n, 1, V), generator=g) < 0.5, 3.2e38, -3.1e38)
+    x = torch.randint(0, V, (n, 1), generator=g)
+    u = torch.rand((n, 2), generator=g) * (1.0 if with_draft else 0.06)
+    tau = float(torch.tensor(3e38, dtype=torch.float32))
+    _compare(t, d if with_draft else None, x, tau, u)

@@ -221,6 +221,11 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify_rows(const VerifyArgs A) 
     if (isinf(m)) {
 #pragma unroll
       for (int j = 0; j < VF_PER; j++) sum += m > 0.f && x[j] == m ? 1.f : 0.f;
+    } else if (m > 1e30f) {
+      // halves: the difference itself may pass fp32's range
+      const float twice = 2.f * fminf(A.per32, 1.5e38f);
+#pragma unroll
+      for (int j = 0; j < VF_PER; j++) sum += exp2_sfu((0.5f * x[j] - 0.5f * m) * twice);
     } else {
 #pragma unroll
       for (int j = 0; j < VF_PER; j++) sum += exp2_sfu((x[j] - m) * A.per32);
