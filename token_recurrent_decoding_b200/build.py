@@ -40,21 +40,34 @@ def sources():
     return out
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
-
-
 def _object(unit: str) -> str:
     return os.path.join(OBJ, os.path.splitext(os.path.basename(unit))[0] + ".o")
 
 
-def _object_stale(unit: str) -> bool:
-    """Whether the unit's object is older than a file of this tree that its last compilation read."""
+def _flags_of(unit: str):
+    """The flags the unit's object was compiled with; None where that is not known."""
+    try:
+        with open(_object(unit) + ".flags") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def stale() -> bool:
+    """Whether the library is older than its sources, or has units of other flags than FLAGS."""
+    if not os.path.exists(LIB):
+        return True
+    t = os.path.getmtime(LIB)
+    return (any(os.path.getmtime(s) > t for s in sources()) or
+            any(_flags_of(u) not in (None, " ".join(FLAGS)) for u in units()))
+
+
+def _object_stale(unit: str, flags) -> bool:
+    """Whether the unit's object has other flags, or is older than a file of this tree that its last
+    compilation read."""
     obj = _object(unit)
-    if not (os.path.exists(obj) and os.path.exists(obj + ".d")):
+    if not (os.path.exists(obj) and os.path.exists(obj + ".d")) or \
+            _flags_of(unit) != " ".join(flags):
         return True
     with open(obj + ".d") as f:
         deps = f.read().replace("\\\n", " ").split()[1:]
@@ -64,19 +77,24 @@ def _object_stale(unit: str) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile the units that changed, side by side, and link them."""
-    if not force and not stale():
+    """Compile the units that changed, side by side, and link them: all of FLAGS and `extra`."""
+    if not force and not extra and not stale():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
-    todo = [u for u in units() if force or extra or _object_stale(u)]
+    flags = [*FLAGS, *extra]
+    todo = [u for u in units() if force or _object_stale(u, flags)]
 
     def compile_unit(unit):
         obj = _object(unit)
-        cmd = [NVCC, *FLAGS, *extra, "-MD", "-MF", obj + ".d", "-c", unit, "-o", obj + ".tmp"]
+        cmd = [NVCC, *flags, "-MD", "-MF", obj + ".d", "-c", unit, "-o", obj + ".tmp"]
         if verbose:
             print(" ".join(cmd), flush=True)
+        if os.path.exists(obj + ".flags"):
+            os.remove(obj + ".flags")
         subprocess.check_call(cmd)
         os.replace(obj + ".tmp", obj)
+        with open(obj + ".flags", "w") as f:
+            f.write(" ".join(flags))
 
     with ThreadPoolExecutor(max(1, min(len(todo), os.cpu_count() or 1))) as pool:
         list(pool.map(compile_unit, todo))
