@@ -257,6 +257,9 @@ def _bad(what: str):
     raise RLTError(1, what)
 
 
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts larger numbers for the C ABI's ints without a word
+
+
 def _ints(t, dev: int, n: int) -> bool:
     """Whether t is a contiguous int32 tensor [n] on GPU `dev`."""
     return (t.dtype is _torch.int32 and t.dim() == 1 and t.size(0) == n and t.is_contiguous()
@@ -352,7 +355,8 @@ class PagedKV:
         n = kv_len.size(0) if kv_len.dim() == 1 else -1
         if not (_ints(kv_len, dev, n) and _ints(cu_rows, dev, n + 1)
                 and table.dtype is _torch.int32 and table.dim() == 2 and table.size(0) == n
-                and table.is_contiguous() and table.get_device() == dev):
+                and table.is_contiguous() and table.get_device() == dev
+                and table.size(1) <= _INT_MAX and rows <= _INT_MAX):
             return None
         if status is not None:
             if not _ints(status, dev, 1):
@@ -402,6 +406,8 @@ def paged_read(cache: PagedKV, table, cu_rows, kv_len, k, v, status=None, stream
 
 def attend_paged_workspace_bytes(cache: PagedKV, n: int, n_heads: int, rows: int, max_rows: int,
                                  max_len: int) -> int:
+    if max(n, n_heads, rows, max_rows, max_len) > _INT_MAX:
+        return 0
     return int(_lib().rlt_attend_paged_workspace_bytes(cache._ref, n, n_heads, rows, max_rows,
                                                        max_len))
 
@@ -427,6 +433,9 @@ def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_l
     r = cache._rows(table, cu_rows, kv_len, rows, status)
     if r is None:
         _bad(what + ": " + _ROWS)
+    if not (0 <= max_rows <= _INT_MAX and 0 <= max_len <= _INT_MAX and 0 <= window <= _INT_MAX
+            and heads <= _INT_MAX):
+        _bad(what + ": max_rows, max_len, window")
     if workspace is None:
         workspace = _empty(stream, cache.device, attend_paged_workspace_bytes(
             cache, r.n, heads, rows, max_rows, max_len), torch.uint8)
@@ -440,6 +449,8 @@ def attend_paged(q, cache: PagedKV, table, cu_rows, kv_len, max_rows: int, max_l
 
 
 def verify_workspace_bytes(n: int, k: int, vocab: int) -> int:
+    if max(n, k, vocab) > _INT_MAX:
+        return 0
     return int(_lib().rlt_verify_workspace_bytes(n, k, vocab))
 
 
@@ -453,6 +464,8 @@ def verify(target, draft, draft_tokens, temperature: float, uniforms=None, draft
     if not (target.dtype is torch.float32 and target.dim() == 3 and dev >= 0):
         _bad(what + ": target float32 [n][k + 1][V] on a GPU")
     n, k, V = target.size(0), target.size(1) - 1, target.size(2)
+    if max(n, k, V) > _INT_MAX:
+        _bad(what + ": sizes")
     t0, t1, t2 = target.stride()
     d0 = d1 = 0
     if t2 != 1 and V != 1:
