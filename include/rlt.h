@@ -553,7 +553,8 @@ typedef struct rlt_paged_kv {
  *   kv_len     [n]: positions of sequence b, its rows of this call included; row
  *              i of m is position kv_len - m + i
  *   n          1 .. RLT_PAGED_MAX_SEQS (2048)
- *   rows       rows of the dense buffers; those behind cu_rows[n] are not touched
+ *   rows       rows of the dense buffers, at most 2^30; those behind cu_rows[n] are
+ *              not touched
  *   status     NULL or a device int32 the kernels OR the bits below into. Nothing
  *              outside the caller's buffers is read or written in any case. */
 #define RLT_PAGED_MAX_SEQS 2048

@@ -89,3 +89,13 @@ def test_verifications_beyond_32_bits_are_refused(cache):
                        counts=Stand(n), workspace=Stand(1 << 20, dtype=torch.uint8))
     assert rlt.verify_workspace_bytes(2, 1, BEYOND) == 0
     assert rlt.verify_workspace_bytes(BEYOND, 1, 8) == 0
+
+
+def test_more_rows_than_blocks_can_number_are_refused():
+    """The C ABI's own int holds them; the grid's size would not."""
+    import ctypes as C
+    c = rlt.rlt_paged_kv(1 << 20, None, 8, 16, 2, 64, 1, 0)
+    for rows_ in (2 ** 31 - 1, 2 ** 30 + 1):
+        r = rlt.rlt_paged_rows(1 << 20, 4, 1 << 20, 1 << 20, 2, rows_, None)
+        for fn in (rlt._lib().rlt_paged_append, rlt._lib().rlt_paged_read):
+            assert fn(C.byref(c), C.byref(r), 1 << 20, 1 << 20, 128, None) == 1

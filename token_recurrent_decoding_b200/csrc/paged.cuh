@@ -57,8 +57,9 @@ inline int paged_args_status(const rlt_paged_kv *c, const rlt_paged_rows *w) {
   if (!w || !c->pages || ((uintptr_t)c->pages & 15)) return RLT_ERR_INVALID_ARG;
   if (c->kind == RLT_KV_E4M3 && (!c->scales || ((uintptr_t)c->scales & 15)))
     return RLT_ERR_INVALID_ARG;
+  // (2^30: block and row numbers stay in 32 bits)
   if (!w->page_table || !w->cu_rows || !w->kv_len || w->table_width < 1 || w->rows < 0 ||
-      w->n < 1 || w->n > RLT_PAGED_MAX_SEQS)
+      w->rows > 1 << 30 || w->n < 1 || w->n > RLT_PAGED_MAX_SEQS)
     return RLT_ERR_INVALID_ARG;
   return RLT_OK;
 }
