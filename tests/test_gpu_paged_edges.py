@@ -248,3 +248,28 @@ def test_the_largest_windows_hide_nothing(kind, m):
     for window in (m - 3, m, m + 1, 2 ** 31 - 1):
         got = rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, short, m, m, window=window)
         assert torch.equal(got, want), window
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_one_row_of_any_stride(kind):
+    """A single row has no stride to speak of: q, k, v and out of odd or different ones."""
+    c = _case(kind, [1], [40], H=2, dh=64, page=16, seed=2).device()
+    want = rlt.attend_paged(c.queries(2).cuda(), c.cache, c.d_table, c.d_cu, c.d_len, 1, 40)
+    c2 = _case(kind, [1], [40], H=2, dh=64, page=16, seed=2).device()
+
+    def odd(x, more):
+        flat = torch.zeros((1, 128 + more), dtype=c.dtype, device="cuda")
+        flat[:, :128] = x.reshape(1, 128)
+        y = flat.as_strided((1, 2, 64), (128 + more, 64, 1))
+        assert y.stride(0) == 128 + more
+        return y
+
+    q = odd(c2.queries(2).cuda(), 3)
+    out = odd(torch.zeros(128, device="cuda"), 5)
+    rlt.attend_paged(q, c2.cache, c2.d_table, c2.d_cu, c2.d_len, 1, 40, out=out)
+    assert torch.equal(out, want)
+    k, v = (torch.randn((1, 2, 64), device="cuda").to(c.dtype) for _ in range(2))
+    rlt.paged_append(c2.cache, c2.d_table, k, odd(v, 7), c2.d_cu, c2.d_len)
+    ko, vo = odd(torch.zeros(128, device="cuda"), 1), torch.zeros_like(v)
+    rlt.paged_read(c2.cache, c2.d_table, c2.d_cu, c2.d_len, ko, vo)
+    assert torch.equal(ko, k) and torch.equal(vo, v)

@@ -366,14 +366,15 @@ class PagedKV:
                               kv_len.data_ptr(), n, rows, status)
 
     def _stride(self, x, heads):
-        """Row stride of dense rows [rows][heads][head_dim], which may lie apart; -1: they do not fit."""
+        """Row stride of dense rows [rows][heads][head_dim], which may lie apart; -1: they do not fit.
+        One row has any: the least is given."""
         if not (x.dtype is self.dtype and x.dim() == 3 and x.size(1) == heads
                 and x.size(2) == self.head_dim and x.get_device() == self._dev):
             return -1
         s0, s1, s2 = x.stride()
         if s2 != 1 or (s1 != self.head_dim and heads != 1):
             return -1
-        return s0 if x.size(0) > 1 else max(s0, heads * self.head_dim)
+        return s0 if x.size(0) > 1 else heads * self.head_dim
 
 
 _ROWS = "page table int32 [n][width], cu_rows int32 [n + 1], kv_len int32 [n] on the cache's GPU"
