@@ -273,3 +273,25 @@ def test_one_row_of_any_stride(kind):
     ko, vo = odd(torch.zeros(128, device="cuda"), 1), torch.zeros_like(v)
     rlt.paged_read(c2.cache, c2.d_table, c2.d_cu, c2.d_len, ko, vo)
     assert torch.equal(ko, k) and torch.equal(vo, v)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dh,heads,H", [(16, 6, 3), (32, 2, 2), (64, 4, 2), (128, 3, 1)])
+def test_queries_that_are_parts_of_wider_rows(kind, dh, heads, H):
+    """q as a fused projection leaves it, on the GPU: row strides of q and out that are neither the
+    rows' own size nor each other's, from steps to chunks of every kernel."""
+    c = _case(kind, [1, 5, 150, 0, 40], [300, 64, 200, 9, 41], H=H, dh=dh, page=16, seed=dh,
+              pad=3).device()
+    wide = torch.randn((c.total, heads + 2 * H, dh), generator=c.g).to(c.dtype).cuda()
+    q = wide[:, H:H + heads]
+    out = torch.full((c.total, heads + 5, dh), 9.0, dtype=c.dtype, device="cuda")
+    assert heads * dh < q.stride(0) != out.stride(0) > heads * dh
+    rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, c.d_len, 150, 300, out=out[:, 2:heads + 2])
+    got, q = out.double().cpu(), q.double().cpu()
+    assert (got[:, :2] == 9).all() and (got[:, heads + 2:] == 9).all()
+    assert (got[int(c.cu[-1]):] == 9).all()
+    for b, m in enumerate(c.rows):
+        lo = int(c.cu[b])
+        ref, _, mass, size = attend64(q[lo:lo + m], c.kv[b], c.lens[b], 0)
+        err = (got[lo:lo + m, 2:heads + 2] - ref).abs()
+        assert (err <= attend_bound(ref, mass, size, dh, c.dtype)).all(), b
