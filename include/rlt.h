@@ -516,7 +516,9 @@ RLT_API int rlt_attend_noalloc(const float *q, const void *kv, const int32_t *h_
  * rlt_paged_append (the chunk's keys and values), rlt_attend_paged (its
  * queries), the head's logits of its rows, rlt_verify; the caller then lowers
  * each sequence's length to what was accepted, and the next append overwrites
- * the refused rows.
+ * the refused rows. That is for layers whose chunk of tokens is computed in one
+ * pass, as a draft model's beside this one; no rlt_model call reads or writes
+ * such a cache, and the decoder's recurrence takes a token a call.
  *
  * A cache, owned by the caller (one per layer):
  *   pages   device, 16-byte aligned, [n_pages][n_kv_heads][2][page_size][head_dim]:
@@ -601,13 +603,18 @@ RLT_API size_t rlt_attend_paged_workspace_bytes(const rlt_paged_kv *cache, int n
  *   lse      NULL or device float32 [rows][n_heads]
  *   n_heads  a multiple of n_kv_heads
  *   max_rows, max_len  host bounds of the rows and positions of one sequence; they
- *            choose kernels and size the workspace
+ *            choose kernels and size the workspace. At most 2^28 each, and rows,
+ *            max_rows times n_heads too. max_rows 0: nothing is done
  *   window   0: no limit
  *   workspace device, 256-byte aligned, owned by the caller; calls that share one
  *            must not overlap
  * A row that sees no key gives zeros and -inf. What lies in keys and values that
- * a row does not see never reaches it; a row that sees a value with an infinity
- * or a NaN among keys that other rows of the chunk do not see becomes NaN. A
+ * a row does not see never reaches it. A row that sees a value with an infinity
+ * or a NaN is not finite in that entry, and where other rows of the chunk do not
+ * see that key the whole row is NaN. Scores, maxima and sums hold 32 bits; in bf16
+ * the weights are rounded to bf16 where they meet the values, as the result is
+ * (error in the norm 1.8e-3, chunks of more than 32 stacked rows 2.3e-3, the
+ * result's own rounding alone 1.7e-3), the log-sum-exp is of the unrounded ones. A
  * row's result does not depend on the batch it is in. Errors: INVALID_ARG (null pointers, sizes,
  * strides or alignment as rlt_paged_append), UNSUPPORTED (head_dim), CAPACITY
  * (workspace too small). */
@@ -628,8 +635,10 @@ RLT_API size_t rlt_verify_workspace_bytes(int n, int k, int vocab);
  *   where that leaves nothing), if none is refused from p_i behind the last one. The draw is the smallest v
  *   whose cumulative weight exceeds uniforms[b][k] * (sum of weights).
  * temperature 0: x_i is accepted if it is the target's first maximum, and the
- * new token is that maximum (draft and uniforms unused). Tests and sums hold 64
- * bits; a weight below 2^-1000 of its row's largest is none. NaN logits count as
+ * new token is that maximum (draft and uniforms unused). Tests and sums are in 64
+ * bits, weights within 2^-42 of themselves (all of a row of logits up to 2^21
+ * temperatures also by one factor within 2^-32, which tests and draws divide out);
+ * one below 2^-1000 of its row's largest is none. NaN logits count as
  * -inf (no weight); where +inf occurs, those entries
  * share the weight. A row without any weight has no token: it ends the
  * sequence's answer there.

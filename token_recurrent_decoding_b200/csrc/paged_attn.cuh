@@ -24,16 +24,21 @@
 // (head_order, col_of), bf16 rows with ldmatrix.
 //
 // Splits: the keys of a sequence are cut into up to 16 ranges when its own
-// (kv head, row tile) pairs are few, by a rule on that sequence alone (cut_seq),
-// so a row's result does not depend on its batch. Ranges are joined in order by
-// k_pattn_merge.
+// (kv head, row tile) pairs are few, by a rule on that sequence alone (cut_seq in
+// paged_plan.h), so a row's result does not depend on its batch. Ranges are joined
+// in order by k_pattn_merge.
+//
+// Weights meet V as bf16 where the operands are bf16: that is the matrix operand,
+// and rounds a result by no more than its own rounding does (a row's heaviest
+// weight so far is one exactly: error in the norm 1.8e-3 against 1.7e-3 of the
+// result's rounding alone). Sums take the unrounded weights, in fp32.
 //
 // Measured on a B200 (device time): one step of 32 sequences of 2000-4096 keys,
-// 16 heads of 128, 8 bits 134-142 us (3 TB/s: bound by issue, about 700
-// instructions per 16 keys and head, half of them turning codes into bf16);
+// 16 heads of 128, 8 bits 134-142 us on two boxes (3 TB/s: bound by issue, about
+// 700 instructions per 16 keys and head, half of them turning codes into bf16);
 // five tokens of 48 sequences of 1000-8192 keys, 32 heads on 8 key heads of
-// 128, bf16 253 us (3.6 TB/s: latency at 8 warps an SM, O of 32 rows takes 128
-// registers); one step of 4 short sequences 10.4 us with the merge.
+// 128, bf16 254 us (3.5 TB/s: latency at 8 warps an SM, O of 32 rows takes 128
+// registers); one step of 4 short sequences 10.7 us with the merge.
 #pragma once
 
 #include <type_traits>

@@ -19,19 +19,24 @@
 //
 // Softmax: O is rescaled (in tensor memory, by the softmax warps) only when a
 // row's maximum has grown by more than 2^8 since the reference it is scaled
-// by; until then weights of up to 2^8 stay exact enough (bf16 has the range,
-// the sum is fp32) and the join divides by the same reference. P's rounding to
-// bf16 is the precision of the matrix operand; sums take the unrounded weights.
+// by; until then weights reach up to 2^8 (bf16 has the range, the sum is fp32)
+// and the join divides by the same reference. P's rounding to bf16 is the
+// precision of the matrix operand, and relative, so the reference does not change
+// it; only that a row's heaviest weight is then rounded like the others, where
+// relative to the maximum it would be one exactly. P's rounding and the result's
+// own, 1.7e-3 in the norm each, make 2.2-2.3e-3 together. Sums take the unrounded
+// weights.
 //
-// Values that some row of the tile does not see are cleared of infinities and
-// NaN by the loaders (0 * NaN would reach that row); a row that does see such
-// a key turns to NaN through its sum.
+// Values that some row of the item does not see are cleared of infinities and
+// NaN by the loaders (0 * NaN would reach that row) and their keys flagged; a row
+// that does see such a key, in a tile that its half may see whole, turns to NaN
+// through its sum.
 //
 // Every mbarrier wait is bounded in device time; a CTA that gives up sets
 // RLT_PAGED_TIMEOUT and leaves.
 //
 // Measured on a B200: 2048 rows behind 30 thousand positions, 16 heads of 128,
-// bf16 580-630 us (850-920 TFLOP/s; 128 of the 148 SMs have a tile). A tile of
+// bf16 610-625 us (850-870 TFLOP/s; 128 of the 148 SMs have a tile). A tile of
 // 256 x 128 scores takes about 3900 clocks against 2048 of the matrix pipe: the
 // chain of one row tile (softmax 1900, PV and scores 1500, hand-overs) sets the
 // pace, not the exponentials or the loads (leaving either out gains 7 %).

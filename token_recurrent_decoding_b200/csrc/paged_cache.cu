@@ -7,9 +7,9 @@
 // 1 <= f < 2, it is x - 8, plus one where f > 1.75 (448 = 1.75 * 2^8). x * 2^-e
 // is exact, so the conversion to e4m3 is the only rounding.
 // Bound by memory; a block takes a few neighbouring rows and finds their
-// sequences once. Measured on a B200: 16 thousand rows of 16 heads of 128 bf16
-// written in 8 bits and read back 91 us (4.4 TB/s), 73 thousand rows of 8 heads
-// read 84 us (5.4 TB/s).
+// sequences once. Measured on a B200 (device time): 16 thousand rows of 16 heads
+// of 128 bf16 written in 8 bits and read back 93 us (4.3 TB/s), 73 thousand rows
+// of 8 heads read 84 us (5.4 TB/s).
 #include <cuda_fp8.h>
 
 #include "paged.cuh"

@@ -34,12 +34,15 @@
 // |f| <= 1/2 (rounded by adding 1.5 * 2^52), 2^(n / 256) from a table of 256
 // entries and the exponent field, 2^(f / 256) from the exponential series to
 // the third power, whose next term is below (ln 2 / 512)^4 / 24 = 1.4e-13.
-// Weights below 2^-1000 are nothing.
+// The maximum's product is rounded for the whole row: one factor within 2^-32.5
+// (products below 2^30; larger ones take exp2) on all its weights and sums, the
+// drafted word's among them, that tests and draws divide out. Weights below
+// 2^-1000 are nothing.
 //
-// Measured on a B200: 64 sequences, up to 5 drafts, 131072 words 97 us
-// (k_verify_rows 33 us, 0.92 of the copy rate; k_verify_draw 64 us, bound by
-// the latency and rate of fp64 operations); 2 sequences of 4 drafts, 32768
-// words 18 us.
+// Measured on a B200 (device time): 64 sequences, up to 5 drafts, 131072 words
+// 94 us (k_verify_rows 33 us, 0.92 of the copy rate; k_verify_draw 61 us: 80
+// registers leave three blocks an SM, 444 places for the 512 blocks, and fp64
+// operations are slow to complete); 2 sequences of 4 drafts, 32768 words 16 us.
 #include <cmath>
 
 #include "paged.cuh"
