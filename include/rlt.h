@@ -599,7 +599,8 @@ RLT_API size_t rlt_attend_paged_workspace_bytes(const rlt_paged_kv *cache, int n
  * to keys max(0, p - window + 1) .. p of head h / (n_heads / n_kv_heads),
  *   out = softmax(q . K_j / sqrt(head_dim)) V_j,  lse = log sum exp(q . K_j / sqrt(head_dim)).
  *   q        device, cache->dtype, [rows][n_heads][head_dim], row stride ldq elements
- *   out      device, cache->dtype, [rows][n_heads][head_dim], row stride ldo
+ *   out      device, cache->dtype, [rows][n_heads][head_dim], row stride ldo; may be
+ *            q itself, of the same stride
  *   lse      NULL or device float32 [rows][n_heads]
  *   n_heads  a multiple of n_kv_heads
  *   max_rows, max_len  host bounds of the rows and positions of one sequence; they

@@ -295,3 +295,87 @@ def test_queries_that_are_parts_of_wider_rows(kind, dh, heads, H):
         ref, _, mass, size = attend64(q[lo:lo + m], c.kv[b], c.lens[b], 0)
         err = (got[lo:lo + m, 2:heads + 2] - ref).abs()
         assert (err <= attend_bound(ref, mass, size, dh, c.dtype)).all(), b
+
+
+# ------------------------------------------------------------- calls at their ends
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,m", [(40, 1), (128, 1), (129, 2), (1024, 1), (64, 5)])
+def test_many_queries_share_one_key_head(kind, heads, m):
+    """One token's heads alone fill the tiles of the many-row kernel."""
+    c = _case(kind, [m, 1, 0], [700, 33, 5], H=1, dh=64, page=64, seed=heads).device()
+    q = c.queries(heads)
+    out = rlt.attend_paged(q.cuda(), c.cache, c.d_table, c.d_cu, c.d_len, m, 700).double().cpu()
+    for b, lo in ((0, 0), (1, m)):
+        ref, _, mass, size = attend64(q[lo:lo + c.rows[b]].double(), c.kv[b], c.lens[b], 0)
+        err = (out[lo:lo + c.rows[b]] - ref).abs()
+        assert (err <= attend_bound(ref, mass, size, 64, c.dtype)).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "bf16e4"])
+@pytest.mark.parametrize("m", [1, 40])
+def test_a_million_positions_on_a_few_pages(kind, m):
+    """Positions past 2^20, every page in the table many times over."""
+    page, L = 1024, 1_000_003
+    c = _case(kind, [m], [16 * page], H=1, dh=64, page=page, seed=m).device()
+    times = -(-L // page)
+    table = c.d_table[:, :16].repeat(1, -(-times // 16))[:, :times].contiguous()
+    kv = c.kv[0].repeat(times // 16 + 1, 1, 1, 1)[:L]
+    q = c.queries(1)
+    n = torch.tensor([L], dtype=torch.int32, device="cuda")
+    out = rlt.attend_paged(q.cuda(), c.cache, table, c.d_cu, n, m, L).double().cpu()
+    rows = [0] if m == 1 else [0, 17, m - 1]
+    for i in rows:
+        last = L - m + i + 1
+        ref, _, mass, size = attend64(q[i:i + 1].double(), kv[:last], last, 0)
+        # a lane adds up to 2 * L / 4096 terms one after the other instead of 512
+        bound = attend_bound(ref, mass, size, 64, c.dtype) + mass * 2.0 ** -23 * L / 2048
+        assert ((out[i:i + 1] - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_output_may_take_the_queries_place(kind):
+    c = _case(kind, [1, 5, 300, 40], [3000, 64, 400, 9000], H=2, dh=64, page=32, seed=6).device()
+    q = c.queries(4).cuda()
+    want = rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, c.d_len, 300, 9000)
+    got = rlt.attend_paged(q, c.cache, c.d_table, c.d_cu, c.d_len, 300, 9000, out=q)
+    assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", [rlt.KV_PLAIN, rlt.KV_E4M3])
+@pytest.mark.parametrize("H,dh,rows", [(1024, 16, 3), (300, 128, 40), (1, 16, 70000)])
+def test_rows_of_many_heads_and_many_rows(kind, H, dh, rows):
+    page = 1024
+    pages = -(-rows // page)
+    cache = rlt.PagedKV.empty(pages, page, H, dh, BF16, kind)
+    g = torch.Generator(device="cuda").manual_seed(H)
+    k, v = (torch.randn((rows, H, dh), generator=g, device="cuda").to(BF16) for _ in range(2))
+    if kind == rlt.KV_E4M3:  # numbers that 8 bits hold: whole, of three bits
+        k, v = (x.float().mul(2).round().clamp(-7, 7).to(BF16) for x in (k, v))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.arange(pages, device="cuda").int().flip(0)[None].contiguous()
+    rlt.paged_append(cache, table, k, v, i32(0, rows), i32(rows))
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    rlt.paged_read(cache, table, i32(0, rows), i32(rows), ko, vo)
+    assert torch.equal(ko, k) and torch.equal(vo, v)
+
+
+def test_a_captured_call_on_a_stream_forked_inside_the_capture():
+    """Calls that make their own buffers, on another stream that joined the capture."""
+    c = _case("bf16", [1, 40], [3000, 900], H=2, dh=64, page=64, seed=1).device()
+    side = torch.cuda.Stream()
+    calls = _calls(c, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        gots = [call() for call, _ in calls]
+        here.wait_stream(side)
+    for _ in range(3):
+        for got in gots:
+            for t in got:
+                t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for got, (_, want) in zip(gots, calls):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
