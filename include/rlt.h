@@ -639,7 +639,9 @@ RLT_API size_t rlt_verify_workspace_bytes(int n, int k, int vocab);
  * new token is that maximum (draft and uniforms unused). Tests and sums are in 64
  * bits, weights within 2^-42 of themselves (all of a row of logits up to 2^21
  * temperatures also by one factor within 2^-32, which tests and draws divide out);
- * one below 2^-1000 of its row's largest is none. NaN logits count as
+ * one below 2^-1000 of its row's largest is none, and differences p - q are known
+ * to about 2^-41 of p (a refused word of rows that both give one word all but 2^-40
+ * of their weight is redrawn from what is left of those). NaN logits count as
  * -inf (no weight); where +inf occurs, those entries
  * share the weight. A row without any weight has no token: it ends the
  * sequence's answer there.
