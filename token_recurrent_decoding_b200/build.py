@@ -4,6 +4,7 @@
 """
 from __future__ import annotations
 
+import contextlib
 import os
 import subprocess
 import sys
@@ -89,7 +90,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         cmd = [NVCC, *flags, "-MD", "-MF", obj + ".d", "-c", unit, "-o", obj + ".tmp"]
         if verbose:
             print(" ".join(cmd), flush=True)
-        if os.path.exists(obj + ".flags"):
+        with contextlib.suppress(FileNotFoundError):  # another build may have
             os.remove(obj + ".flags")
         subprocess.check_call(cmd)
         os.replace(obj + ".tmp", obj)
